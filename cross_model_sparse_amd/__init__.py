@@ -14,3 +14,8 @@ from .mapflow import (  # noqa: F401
     MF_OK, MF_ERR_INVALID, MF_ERR_UNSUPPORTED, MF_ERR_CAPACITY, MF_ERR_HIP,
     MF_F32, MF_F16, MF_BF16,
 )
+from .attention import (  # noqa: F401
+    rope_frequencies, qk_norm_rope, attention_window, attention_window_varlen,
+    attention_split_workspace_bytes, attention_decode, attention_decode_workspace_bytes,
+    key_mass_qk, key_mass_qk_workspace_bytes, cache_evict,
+)

@@ -1,0 +1,182 @@
+// Cache eviction by accumulated mass: selection and compaction.
+//
+// k_evict_select, one workgroup per (sequence, KV head): the budget-th largest
+// mass is found digit by digit on order-preserving integer keys (four 8-bit
+// histograms over the row, which stays in L2), then the kept rows are written
+// in ascending order: each wavefront owns a contiguous run of rows, counts its
+// rows above the threshold and at it, and after one prefix over the wavefronts
+// places its own by ballots.  Rows at the threshold are taken lowest first.
+// k_evict_gather copies the kept rows, 16 bytes a lane: every kept row is read
+// once and written once.
+#include "mf_attn.h"
+
+#include <algorithm>
+
+namespace {
+
+using namespace mfd;
+
+constexpr int kSelThreads = 1024;
+constexpr int kSelWaves = kSelThreads / 64;
+
+// larger mass -> larger key; NaN counts as -infinity, -0 as 0
+__device__ __forceinline__ unsigned mass_key(float f) {
+  if (f != f) f = -INFINITY;
+  f += 0.f;                                     // -0 -> +0
+  const unsigned u = __float_as_uint(f);
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+__global__ __launch_bounds__(kSelThreads) void k_evict_select(const mf::EvictArgs a) {
+  __shared__ unsigned hist[kSelWaves][256];
+  __shared__ unsigned above_w[kSelWaves], tie_w[kSelWaves];
+  __shared__ unsigned s_digit, s_left;
+  const int sg = blockIdx.x;
+  const int s = sg / a.H_kv;
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int len = cache_len(a.c, s);
+  const int n = min(len, a.budget);
+  const float* mass = a.mass + (int64_t)sg * a.ldmass;
+  int32_t* kept = a.kept + (int64_t)sg * a.budget;
+  float* mo = a.mass_out ? a.mass_out + (int64_t)sg * a.cap_out : nullptr;
+  if (t == 0 && a.lens_out && sg % a.H_kv == 0) a.lens_out[s] = n;
+  for (int64_t r = n + t; r < a.budget; r += kSelThreads) kept[r] = -1;
+  if (mo)
+    for (int64_t r = n + t; r < a.cap_out; r += kSelThreads) mo[r] = 0.f;
+  if (len <= a.budget) {
+    for (int r = t; r < n; r += kSelThreads) {
+      kept[r] = r;
+      if (mo) mo[r] = mass[r];
+    }
+    return;
+  }
+  // first tokens and last tokens, whatever their mass
+  for (int r = t; r < a.sinks; r += kSelThreads) {
+    kept[r] = r;
+    if (mo) mo[r] = mass[r];
+  }
+  for (int r = t; r < a.recent; r += kSelThreads) {
+    kept[n - a.recent + r] = len - a.recent + r;
+    if (mo) mo[n - a.recent + r] = mass[len - a.recent + r];
+  }
+  const int c0 = a.sinks, c1 = len - a.recent;  // candidates
+  unsigned want = n - a.sinks - a.recent;       // < c1 - c0, since len > budget
+  if (want == 0) return;
+
+  unsigned prefix = 0;                          // digits found so far
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = t; i < kSelWaves * 256; i += kSelThreads) (&hist[0][0])[i] = 0;
+    __syncthreads();
+    const unsigned hi = shift == 24 ? 0u : ~0u << (shift + 8);
+    for (int j = c0 + t; j < c1; j += kSelThreads) {
+      const unsigned k = mass_key(mass[j]);
+      if ((k & hi) == prefix) atomicAdd(&hist[wave][(k >> shift) & 255], 1u);
+    }
+    __syncthreads();
+    if (t < 256) {
+      unsigned v = 0;
+      for (int w = 0; w < kSelWaves; ++w) v += hist[w][t];
+      hist[0][t] = v;
+    }
+    __syncthreads();
+    if (t == 0) {
+      unsigned left = want;
+      int dgt = 255;
+      for (; dgt > 0; --dgt) {
+        const unsigned v = hist[0][dgt];
+        if (v >= left) break;
+        left -= v;
+      }
+      s_digit = dgt;
+      s_left = left;
+    }
+    __syncthreads();
+    prefix |= s_digit << shift;
+    want = s_left;                              // still to take among this prefix
+    __syncthreads();
+  }
+  // keys above `prefix` are kept, and the first `want` rows equal to it
+  const int seg = (((c1 - c0) + kSelWaves - 1) / kSelWaves + 63) / 64 * 64;
+  const int64_t b0 = (int64_t)c0 + (int64_t)wave * seg;
+  const int w0 = (int)min(b0, (int64_t)c1), w1 = (int)min(b0 + seg, (int64_t)c1);
+  unsigned na = 0, nt = 0;
+  for (int j = w0; j < w1; j += 64) {
+    const unsigned k = j + lane < w1 ? mass_key(mass[j + lane]) : 0u;
+    const bool in = j + lane < w1;
+    na += __popcll(__ballot(in && k > prefix));
+    nt += __popcll(__ballot(in && k == prefix));
+  }
+  if (lane == 0) { above_w[wave] = na; tie_w[wave] = nt; }
+  __syncthreads();
+  unsigned ties = 0, out = a.sinks;
+  for (int w = 0; w < wave; ++w) {
+    out += above_w[w] + (min(ties + tie_w[w], want) - min(ties, want));
+    ties += tie_w[w];
+  }
+  const uint64_t below = (1ull << lane) - 1;
+  for (int j = w0; j < w1; j += 64) {
+    const bool in = j + lane < w1;
+    const float m = in ? mass[j + lane] : 0.f;
+    const unsigned k = mass_key(m);
+    const uint64_t bt = __ballot(in && k == prefix);
+    const bool keep = in && (k > prefix || (k == prefix && ties + __popcll(bt & below) < want));
+    const uint64_t bk = __ballot(keep);
+    if (keep) {
+      const unsigned o = out + __popcll(bk & below);
+      kept[o] = j + lane;
+      if (mo) mo[o] = m;
+    }
+    out += __popcll(bk);
+    ties += __popcll(bt);
+  }
+}
+
+// grid (row chunk, sequence * H_kv); a lane moves 16 bytes of K and of V
+template <int kRowBytes>
+__global__ __launch_bounds__(256) void k_evict_gather(const mf::EvictArgs a, int es) {
+  constexpr int LPR = kRowBytes / 16;
+  constexpr int RPB = 256 / LPR;
+  const int sg = blockIdx.y;
+  const int s = sg / a.H_kv, g = sg - s * a.H_kv;
+  const int n = min(cache_len(a.c, s), a.budget);
+  const int r = blockIdx.x * RPB + threadIdx.x / LPR;
+  const int b = 16 * (threadIdx.x % LPR);
+  if (r >= n) return;
+  const int j = a.kept[(int64_t)sg * a.budget + r];
+  const int64_t src = cache_row(a.c, s, j, g, a.H_kv, a.d);
+  const int64_t dst = ((int64_t)sg * a.cap_out + r) * kRowBytes + b;
+  uint4 k = make_uint4(0, 0, 0, 0), v = k;
+  if (src >= 0) {
+    k = *reinterpret_cast<const uint4*>((const char*)a.c.K + src * es + b);
+    v = *reinterpret_cast<const uint4*>((const char*)a.c.V + src * es + b);
+  }
+  *reinterpret_cast<uint4*>((char*)a.K_out + dst) = k;
+  *reinterpret_cast<uint4*>((char*)a.V_out + dst) = v;
+}
+
+template <int RB>
+void gather(const mf::EvictArgs& a, int es, int rows, hipStream_t st) {
+  constexpr int RPB = 256 / (RB / 16);
+  const dim3 grid((rows + RPB - 1) / RPB, a.S * a.H_kv);
+  k_evict_gather<RB><<<grid, 256, 0, st>>>(a, es);
+}
+
+}  // namespace
+
+namespace mf {
+
+hipError_t launch_evict(int dt, const EvictArgs& a, hipStream_t st) {
+  k_evict_select<<<a.S * a.H_kv, kSelThreads, 0, st>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int es = dtype_bytes(dt), rows = std::min(a.budget, a.c.max_len);
+  if (rows == 0) return hipSuccess;
+  switch (a.d * es) {
+    case 128: gather<128>(a, es, rows, st); break;
+    case 256: gather<256>(a, es, rows, st); break;
+    default: gather<512>(a, es, rows, st); break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace mf

@@ -7,7 +7,7 @@
 #include <mutex>
 #include <string>
 
-#include "mf_internal.h"
+#include "mf_attn.h"
 
 // Fixed scratch of mf_topp_select_bsr_noalloc: the selection's kept[T][T] and
 // count[T] int32 arrays for up to kNoAllocMaxT block rows.  Each GPU the
@@ -445,6 +445,325 @@ int mf_retrieve_fused_varlen(int S, int R, const int32_t* cu_seqlens, const int3
   return mf::launch_retrieve_varlen(S, R, cu_seqlens, cu_rows, row_ptr, col_idx, block_table, vals,
                                     n_pages, nnzb, dtype, H_s, B, W, H_r, V, H_kv, d, ldV, O, ldO,
                                     (hipStream_t)stream);
+}
+
+// ---- attention operators --------------------------------------------------
+
+#define MF_REQUIRE(cond, msg) \
+  do {                        \
+    if (!(cond)) return mf::fail(MF_ERR_INVALID, std::string(fn) + ": " + (msg)); \
+  } while (0)
+
+static int check_heads(const char* fn, int dtype, int H, int H_kv, int d) {
+  MF_REQUIRE(valid_dtype(dtype), fmt("unknown dtype code %lld", dtype));
+  MF_REQUIRE(H >= 1 && H <= 64, fmt("head counts must be in [1, 64] (got %lld)", H));
+  MF_REQUIRE(H_kv >= 1 && H % H_kv == 0, fmt("H = %lld is not a multiple of H_kv = %lld", H, H_kv));
+  MF_REQUIRE(d == 64 || d == 128, fmt("d must be 64 or 128 (got %lld)", d));
+  return MF_OK;
+}
+
+static int check_workspace(const char* fn, const void* ws, size_t have, size_t need) {
+  MF_REQUIRE(need == 0 || (ws && have >= need),
+             fmt("workspace of %lld bytes < %lld required", ws ? (long long)have : 0LL,
+                 (long long)need));
+  MF_REQUIRE(!ws || reinterpret_cast<uintptr_t>(ws) % 16 == 0, "workspace off 16 bytes");
+  return MF_OK;
+}
+
+// strides of an output that keep its N x H rows of d elements apart
+static bool rows_apart(int64_t N, int64_t H, int64_t d, int64_t ld, int64_t hs) {
+  const bool by_row = hs >= d && ld >= (H - 1) * hs + d;
+  const bool by_head = ld >= d && hs >= (N - 1) * ld + d;
+  return by_row || by_head || (N <= 1 && hs >= d) || (H <= 1 && ld >= d);
+}
+
+static int check_mask(const char* fn, int window, int sinks) {
+  MF_REQUIRE(window >= 0, fmt("window must be >= 0 (got %lld)", window));
+  MF_REQUIRE(sinks >= 0, fmt("sinks must be >= 0 (got %lld)", sinks));
+  return MF_OK;
+}
+
+static int check_cache(const char* fn, const mf::Cache& c, int S, bool empty) {
+  MF_REQUIRE(S >= 0, "S < 0");
+  MF_REQUIRE(c.n_pages >= 0, "n_pages < 0");
+  MF_REQUIRE(c.page >= 1, fmt("page must be >= 1 (got %lld)", c.page));
+  MF_REQUIRE(c.max_pages >= 0, "max_pages < 0");
+  MF_REQUIRE(c.max_len >= 0 && c.max_len <= (int64_t)c.max_pages * c.page,
+             fmt("max_len = %lld outside [0, max_pages*page = %lld]", c.max_len,
+                 (long long)c.max_pages * c.page));
+  if (empty) return MF_OK;
+  MF_REQUIRE(c.lens, "null lens");
+  MF_REQUIRE((c.K && c.V) || c.n_pages == 0 || c.max_len == 0, "null pool");
+  MF_REQUIRE(reinterpret_cast<uintptr_t>(c.K) % 16 == 0 && reinterpret_cast<uintptr_t>(c.V) % 16 == 0,
+             "pools must be 16-byte aligned");
+  return MF_OK;
+}
+
+int mf_rope_frequencies(int rot, double base, int scaling, double factor, double orig_len,
+                        double beta_fast, double beta_slow, double* freq, double* attn_factor) {
+  const char* fn = "mf_rope_frequencies";
+  MF_REQUIRE(freq && attn_factor, "null pointer");
+  MF_REQUIRE(rot >= 2 && rot <= 256 && rot % 2 == 0, fmt("rot must be even and in [2, 256] (got %lld)", rot));
+  MF_REQUIRE(base > 1.0 && isfinite(base), "base must be > 1");
+  MF_REQUIRE(factor >= 1.0 && isfinite(factor), "factor must be >= 1");
+  MF_REQUIRE(scaling >= MF_ROPE_PLAIN && scaling <= MF_ROPE_YARN, fmt("unknown scaling %lld", scaling));
+  MF_REQUIRE(scaling != MF_ROPE_NTK || rot > 2, "rot must be > 2 for this scaling");
+  double lo = 0, hi = 0;
+  if (scaling == MF_ROPE_YARN) {
+    MF_REQUIRE(orig_len > 0 && isfinite(orig_len), "orig_len must be > 0");
+    MF_REQUIRE(beta_slow > 0 && beta_fast > beta_slow && isfinite(beta_fast), "need 0 < beta_slow < beta_fast");
+    const double two_pi = 6.283185307179586476925;
+    lo = floor(rot * log(orig_len / (beta_fast * two_pi)) / (2 * log(base)));
+    hi = ceil(rot * log(orig_len / (beta_slow * two_pi)) / (2 * log(base)));
+    lo = lo < 0 ? 0 : lo;
+    hi = hi > rot - 1 ? rot - 1 : hi;
+  }
+  if (scaling == MF_ROPE_NTK) base *= pow(factor, rot / (rot - 2.0));
+  for (int i = 0; i < rot / 2; ++i) {
+    double f = pow(base, -2.0 * i / rot);
+    if (scaling == MF_ROPE_LINEAR) f /= factor;
+    if (scaling == MF_ROPE_YARN) {
+      const double span = hi - lo > 0.001 ? hi - lo : 0.001;
+      double r = (i - lo) / span;
+      r = r < 0 ? 0 : r > 1 ? 1 : r;
+      f = f / factor * r + f * (1 - r);
+    }
+    freq[i] = f;
+  }
+  *attn_factor = scaling == MF_ROPE_YARN ? 0.1 * log(factor) + 1.0 : 1.0;
+  return MF_OK;
+}
+
+static int check_rope(const char* fn, int dtype, const mf::RopeArgs& a) {
+  MF_REQUIRE(valid_dtype(dtype), fmt("unknown dtype code %lld", dtype));
+  MF_REQUIRE(a.N >= 0, "N < 0");
+  MF_REQUIRE(a.d == 64 || a.d == 128, fmt("d must be 64 or 128 (got %lld)", a.d));
+  MF_REQUIRE(a.H_q >= 1 && a.H_q <= 64 && a.H_k >= 1 && a.H_k <= 64, "head counts must be in [1, 64]");
+  MF_REQUIRE(a.rot >= 0 && a.rot <= a.d && a.rot % 2 == 0, fmt("rot must be even and in [0, d] (got %lld)", a.rot));
+  MF_REQUIRE(a.layout == MF_ROPE_HALF || a.layout == MF_ROPE_INTERLEAVED, fmt("unknown layout %lld", a.layout));
+  MF_REQUIRE(a.eps >= 0.f, "eps must be >= 0");
+  MF_REQUIRE(a.ldq >= (int64_t)a.H_q * a.d && a.ldk >= (int64_t)a.H_k * a.d, "ldq or ldk smaller than a row");
+  MF_REQUIRE(rows_apart(a.N, a.H_q, a.d, a.ldQ, a.hsQ), "rows of Q overlap");
+  if (a.N == 0) return MF_OK;
+  MF_REQUIRE(a.q && a.k && a.Q, "null pointer");
+  MF_REQUIRE(a.rot == 0 || (a.freq && a.positions), "null freq or positions");
+  return MF_OK;
+}
+
+int mf_qk_norm_rope(int dtype, int N, int d, const void* q, int H_q, int64_t ldq, const void* k,
+                    int H_k, int64_t ldk, const void* wq, const void* wk, float eps,
+                    const double* freq, int rot, int layout, float attn_factor,
+                    const int32_t* positions, void* Q, int64_t ldQ, int64_t hsQ, void* K,
+                    int64_t ldK, int64_t hsK, void* stream) {
+  const char* fn = "mf_qk_norm_rope";
+  mf::RopeArgs a = {};
+  a.N = N; a.d = d; a.H_q = H_q; a.H_k = H_k;
+  a.q = q; a.k = k; a.ldq = ldq; a.ldk = ldk;
+  a.wq = wq; a.wk = wk; a.eps = eps;
+  a.freq = freq; a.rot = rot; a.layout = layout; a.attn_factor = attn_factor;
+  a.positions = positions;
+  a.Q = Q; a.K = K; a.ldQ = ldQ; a.hsQ = hsQ; a.ldK = ldK; a.hsK = hsK;
+  const int st = check_rope(fn, dtype, a);
+  if (st != MF_OK) return st;
+  MF_REQUIRE(rows_apart(N, H_k, d, ldK, hsK), "rows of K overlap");
+  if (N == 0) return MF_OK;
+  MF_REQUIRE(K && K != Q, "null K, or K equal to Q");
+  MF_REQUIRE((Q != q || (ldQ == ldq && hsQ == d)) && (K != k || (ldK == ldk && hsK == d)) && Q != k && K != q,
+             "an output overlaps an input with another layout");
+  return mf::hip_check(mf::launch_rope(dtype, a, (hipStream_t)stream), "mf_qk_norm_rope launch");
+}
+
+int mf_qk_norm_rope_cache(int dtype, int N, int d, const void* q, int H_q, int64_t ldq,
+                          const void* k, int H_k, int64_t ldk, const void* v, int64_t ldv,
+                          const void* wq, const void* wk, float eps, const double* freq, int rot,
+                          int layout, float attn_factor, const int32_t* positions, void* Q,
+                          int64_t ldQ, int64_t hsQ, const int64_t* slots, void* K, void* V,
+                          int64_t n_pages, int page, void* stream) {
+  const char* fn = "mf_qk_norm_rope_cache";
+  mf::RopeArgs a = {};
+  a.N = N; a.d = d; a.H_q = H_q; a.H_k = H_k;
+  a.q = q; a.k = k; a.v = v; a.ldq = ldq; a.ldk = ldk; a.ldv = ldv;
+  a.wq = wq; a.wk = wk; a.eps = eps;
+  a.freq = freq; a.rot = rot; a.layout = layout; a.attn_factor = attn_factor;
+  a.positions = positions;
+  a.Q = Q; a.K = K; a.V = V; a.ldQ = ldQ; a.hsQ = hsQ;
+  a.slots = slots; a.n_pages = n_pages; a.page = page;
+  const int st = check_rope(fn, dtype, a);
+  if (st != MF_OK) return st;
+  MF_REQUIRE(ldv >= (int64_t)H_k * d, "ldv smaller than a row");
+  MF_REQUIRE(n_pages >= 0 && page >= 1, "n_pages < 0 or page < 1");
+  if (N == 0) return MF_OK;
+  MF_REQUIRE(v && slots, "null v or slots");
+  MF_REQUIRE((K && V) || n_pages == 0, "null pool");
+  MF_REQUIRE(reinterpret_cast<uintptr_t>(K) % 16 == 0 && reinterpret_cast<uintptr_t>(V) % 16 == 0,
+             "pools must be 16-byte aligned");
+  MF_REQUIRE(n_pages == 0 || K != V, "K and V are one pool");
+  MF_REQUIRE((Q != q || (ldQ == ldq && hsQ == d)) && Q != k && Q != v,
+             "an output overlaps an input with another layout");
+  return mf::hip_check(mf::launch_rope(dtype, a, (hipStream_t)stream), "mf_qk_norm_rope_cache launch");
+}
+
+static int check_attention(const char* fn, int dtype, const mf::AttnArgs& a) {
+  int st = check_heads(fn, dtype, a.H, a.H_kv, a.d);
+  if (st != MF_OK) return st;
+  MF_REQUIRE(a.N_q >= 0 && a.N_k >= 0, "N_q or N_k < 0");
+  st = check_mask(fn, a.window, a.sinks);
+  if (st != MF_OK) return st;
+  MF_REQUIRE(a.Q.ld >= 0 && a.Q.hs >= 0 && a.K.ld >= 0 && a.K.hs >= 0 && a.V.ld >= 0 && a.V.hs >= 0,
+             "a stride is negative");
+  MF_REQUIRE(a.ldO >= (int64_t)a.H * a.d, "ldO < H*d");
+  if (a.N_q == 0) return MF_OK;
+  MF_REQUIRE(a.Q.p && a.O && a.scale && ((a.K.p && a.V.p) || a.N_k == 0), "null pointer");
+  MF_REQUIRE(a.O != a.Q.p && a.O != a.K.p && a.O != a.V.p, "O is one of the inputs");
+  return MF_OK;
+}
+
+size_t mf_attention_split_workspace_bytes(int dtype, int H, int H_kv, int N_q, int N_k, int d,
+                                          int window, int sinks) {
+  if (!valid_dtype(dtype) || H < 1 || H > 64 || H_kv < 1 || H % H_kv != 0 || (d != 64 && d != 128) ||
+      N_q < 1 || N_k < 1 || window < 0 || sinks < 0)
+    return 0;
+  return mf::attention_split_bytes(dtype, H, H_kv, N_q, N_k, d, window, sinks);
+}
+
+int mf_attention_window(const void* Q, int64_t ldQ, int64_t hsQ, const void* K, int64_t ldK,
+                        int64_t hsK, const void* V, int64_t ldV, int64_t hsV, int dtype, int H,
+                        int H_kv, int N_q, int N_k, int d, const float* scale, int window,
+                        int sinks, void* O, int64_t ldO, float* lse, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  const char* fn = "mf_attention_window";
+  mf::AttnArgs a = {};
+  a.Q = {Q, ldQ, hsQ}; a.K = {K, ldK, hsK}; a.V = {V, ldV, hsV};
+  a.O = O; a.ldO = ldO; a.lse = lse; a.scale = scale;
+  a.H = H; a.H_kv = H_kv; a.N_q = N_q; a.N_k = N_k; a.d = d; a.window = window; a.sinks = sinks;
+  int st = check_attention(fn, dtype, a);
+  if (st != MF_OK || N_q == 0) return st;
+  st = check_workspace(fn, workspace, workspace_bytes, 0);
+  if (st != MF_OK) return st;
+  return mf::hip_check(mf::launch_attention(dtype, a, workspace, workspace ? workspace_bytes : 0,
+                                            (hipStream_t)stream), "mf_attention_window launch");
+}
+
+int mf_attention_window_varlen(int S, const int32_t* cu_q, const int32_t* cu_k, const void* Q,
+                               int64_t ldQ, int64_t hsQ, const void* K, int64_t ldK, int64_t hsK,
+                               const void* V, int64_t ldV, int64_t hsV, int dtype, int H, int H_kv,
+                               int N_q, int N_k, int d, const float* scale, int window, int sinks,
+                               void* O, int64_t ldO, float* lse, void* stream) {
+  const char* fn = "mf_attention_window_varlen";
+  mf::AttnArgs a = {};
+  a.Q = {Q, ldQ, hsQ}; a.K = {K, ldK, hsK}; a.V = {V, ldV, hsV};
+  a.O = O; a.ldO = ldO; a.lse = lse; a.scale = scale;
+  a.H = H; a.H_kv = H_kv; a.N_q = N_q; a.N_k = N_k; a.d = d; a.window = window; a.sinks = sinks;
+  a.S = S; a.cu_q = cu_q; a.cu_k = cu_k;
+  MF_REQUIRE(S >= 0, fmt("S must be >= 0 (got %lld)", S));
+  const int st = check_attention(fn, dtype, a);
+  if (st != MF_OK || N_q == 0 || S == 0) return st;
+  MF_REQUIRE(cu_q && cu_k, "null cu_q or cu_k");
+  return mf::hip_check(mf::launch_attention(dtype, a, nullptr, 0, (hipStream_t)stream),
+                       "mf_attention_window_varlen launch");
+}
+
+size_t mf_attention_decode_workspace_bytes(int S, int max_len, int H, int H_kv, int d, int window,
+                                           int sinks, int with_mass) {
+  if (S < 1 || max_len < 0 || H < 1 || H > 64 || H_kv < 1 || H % H_kv != 0 || (d != 64 && d != 128) ||
+      window < 0 || sinks < 0)
+    return 0;
+  return mf::decode_workspace_bytes(S, max_len, H, H_kv, d, window, sinks, with_mass != 0);
+}
+
+int mf_attention_decode(const void* Q, int64_t ldQ, const void* K, const void* V, int64_t n_pages,
+                        int page, const int32_t* block_table, int max_pages, const int32_t* lens,
+                        int dtype, int S, int max_len, int H, int H_kv, int d, const float* scale,
+                        int window, int sinks, void* O, int64_t ldO, float* lse,
+                        const float* mass_in, float* mass_out, int64_t ldmass, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  const char* fn = "mf_attention_decode";
+  mf::DecodeArgs a = {};
+  a.Q = Q; a.ldQ = ldQ;
+  a.c = {K, V, n_pages, page, block_table, max_pages, lens, max_len};
+  a.S = S; a.H = H; a.H_kv = H_kv; a.d = d; a.window = window; a.sinks = sinks;
+  a.scale = scale; a.O = O; a.ldO = ldO; a.lse = lse;
+  a.mass_in = mass_in; a.mass_out = mass_out; a.ldmass = ldmass;
+  int st = check_heads(fn, dtype, H, H_kv, d);
+  if (st != MF_OK) return st;
+  st = check_mask(fn, window, sinks);
+  if (st != MF_OK) return st;
+  st = check_cache(fn, a.c, S, S == 0);
+  if (st != MF_OK) return st;
+  MF_REQUIRE(ldQ >= (int64_t)H * d && ldO >= (int64_t)H * d, "ldQ or ldO < H*d");
+  MF_REQUIRE(!mass_in || mass_out, "mass_in without mass_out");
+  MF_REQUIRE(!mass_out || ldmass >= max_len, "ldmass < max_len");
+  if (S == 0) return MF_OK;
+  MF_REQUIRE(Q && O && scale, "null pointer");
+  MF_REQUIRE(O != Q && O != K && O != V, "O is one of the inputs");
+  st = check_workspace(fn, workspace, workspace_bytes,
+                       mf::decode_workspace_bytes(S, max_len, H, H_kv, d, window, sinks, mass_out != nullptr));
+  if (st != MF_OK) return st;
+  return mf::hip_check(mf::launch_decode(dtype, a, workspace, (hipStream_t)stream),
+                       "mf_attention_decode launch");
+}
+
+size_t mf_key_mass_qk_workspace_bytes(int dtype, int H, int H_kv, int N_q, int N_k, int d,
+                                      int window, int sinks) {
+  if (!valid_dtype(dtype) || H < 1 || H > 64 || H_kv < 1 || H % H_kv != 0 || (d != 64 && d != 128) ||
+      N_q < 0 || N_k < 0 || window < 0 || sinks < 0)
+    return 0;
+  return mf::key_mass_workspace_bytes(dtype, H, H_kv, N_q, N_k, d, window, sinks);
+}
+
+int mf_key_mass_qk(const void* Q, int64_t ldQ, int64_t hsQ, const void* K, int64_t ldK, int64_t hsK,
+                   const float* scale, const float* lse, int dtype, int H, int H_kv, int N_q,
+                   int N_k, int d, int window, int sinks, const float* mass_in, float* mass_out,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "mf_key_mass_qk";
+  mf::KeyMassArgs a = {};
+  a.Q = {Q, ldQ, hsQ}; a.K = {K, ldK, hsK}; a.scale = scale; a.lse = lse;
+  a.H = H; a.H_kv = H_kv; a.N_q = N_q; a.N_k = N_k; a.d = d; a.window = window; a.sinks = sinks;
+  a.mass_in = mass_in; a.mass_out = mass_out;
+  int st = check_heads(fn, dtype, H, H_kv, d);
+  if (st != MF_OK) return st;
+  MF_REQUIRE(N_q >= 0 && N_k >= 0, "N_q or N_k < 0");
+  st = check_mask(fn, window, sinks);
+  if (st != MF_OK) return st;
+  MF_REQUIRE(ldQ >= 0 && hsQ >= 0 && ldK >= 0 && hsK >= 0, "a stride is negative");
+  if (N_k == 0) return MF_OK;
+  MF_REQUIRE(K && scale && mass_out && ((Q && lse) || N_q == 0), "null pointer");
+  st = check_workspace(fn, workspace, workspace_bytes,
+                       mf::key_mass_workspace_bytes(dtype, H, H_kv, N_q, N_k, d, window, sinks));
+  if (st != MF_OK) return st;
+  return mf::hip_check(mf::launch_key_mass(dtype, a, workspace, (hipStream_t)stream),
+                       "mf_key_mass_qk launch");
+}
+
+int mf_cache_evict(const float* mass, int64_t ldmass, const void* K, const void* V, int64_t n_pages,
+                   int page, const int32_t* block_table, int max_pages, const int32_t* lens,
+                   int dtype, int S, int max_len, int H_kv, int d, int budget, int sinks,
+                   int recent, void* K_out, void* V_out, int64_t cap_out, float* mass_out,
+                   int32_t* kept, int32_t* lens_out, void* stream) {
+  const char* fn = "mf_cache_evict";
+  mf::EvictArgs a = {};
+  a.mass = mass; a.ldmass = ldmass;
+  a.c = {K, V, n_pages, page, block_table, max_pages, lens, max_len};
+  a.S = S; a.H_kv = H_kv; a.d = d; a.budget = budget; a.sinks = sinks; a.recent = recent;
+  a.K_out = K_out; a.V_out = V_out; a.cap_out = cap_out; a.mass_out = mass_out;
+  a.kept = kept; a.lens_out = lens_out;
+  int st = check_heads(fn, dtype, H_kv, H_kv, d);
+  if (st != MF_OK) return st;
+  st = check_cache(fn, a.c, S, S == 0);
+  if (st != MF_OK) return st;
+  MF_REQUIRE(budget >= 1, fmt("budget must be >= 1 (got %lld)", budget));
+  MF_REQUIRE(sinks >= 0 && recent >= 0 && (int64_t)sinks + recent <= budget,
+             "sinks and recent must be >= 0 and together at most budget");
+  MF_REQUIRE(cap_out >= budget, "cap_out < budget");
+  MF_REQUIRE(ldmass >= max_len, "ldmass < max_len");
+  if (S == 0) return MF_OK;
+  MF_REQUIRE((mass || max_len == 0) && kept && K_out && V_out, "null pointer");
+  MF_REQUIRE(reinterpret_cast<uintptr_t>(K_out) % 16 == 0 && reinterpret_cast<uintptr_t>(V_out) % 16 == 0,
+             "pools must be 16-byte aligned");
+  MF_REQUIRE(K_out != K && K_out != V && V_out != K && V_out != V && K_out != V_out,
+             "an output pool is a source pool or the other output");
+  MF_REQUIRE(mass_out != mass || !mass, "mass_out is mass");
+  return mf::hip_check(mf::launch_evict(dtype, a, (hipStream_t)stream), "mf_cache_evict launch");
 }
 
 }  // extern "C"

@@ -31,7 +31,12 @@ EXPORTED = ("mf_abi_version", "mf_status_string", "mf_last_error", "mf_block_mas
             "mf_retrieve_fused",
             "mf_retrieve_fused_multi", "mf_retrieve_fused_varlen", "mf_prefix_hashes",
             "mf_bm_create", "mf_bm_destroy", "mf_bm_lookup", "mf_bm_release", "mf_bm_insert",
-            "mf_bm_stats", "mf_pool_store")
+            "mf_bm_stats", "mf_pool_store",
+            "mf_rope_frequencies", "mf_qk_norm_rope", "mf_qk_norm_rope_cache",
+            "mf_attention_window", "mf_attention_split_workspace_bytes",
+            "mf_attention_window_varlen", "mf_attention_decode_workspace_bytes",
+            "mf_attention_decode", "mf_key_mass_qk_workspace_bytes", "mf_key_mass_qk",
+            "mf_cache_evict")
 
 
 class MapflowError(RuntimeError):
@@ -138,6 +143,40 @@ def load() -> ctypes.CDLL:
     L.mf_retrieve_fused_varlen.argtypes = [c_int, c_int, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
                                            c_i64, c_i64, c_int, c_int, c_int, c_vp, c_int,
                                            c_vp, c_int, c_int, c_i64, c_vp, c_i64, c_vp]
+    c_d = ctypes.c_double
+    L.mf_rope_frequencies.restype = c_int
+    L.mf_rope_frequencies.argtypes = [c_int, c_d, c_int, c_d, c_d, c_d, c_d, c_vp, c_vp]
+    rope = [c_int, c_int, c_int, c_vp, c_int, c_i64, c_vp, c_int, c_i64]
+    norm = [c_vp, c_vp, c_f, c_vp, c_int, c_int, c_f, c_vp, c_vp, c_i64, c_i64]
+    L.mf_qk_norm_rope.restype = c_int
+    L.mf_qk_norm_rope.argtypes = rope + norm + [c_vp, c_i64, c_i64, c_vp]
+    L.mf_qk_norm_rope_cache.restype = c_int
+    L.mf_qk_norm_rope_cache.argtypes = (rope + [c_vp, c_i64] + norm +
+                                        [c_vp, c_vp, c_vp, c_i64, c_int, c_vp])
+    rows = [c_vp, c_i64, c_i64]
+    L.mf_attention_window.restype = c_int
+    L.mf_attention_window.argtypes = (rows * 3 + [c_int] * 6 + [c_vp, c_int, c_int, c_vp, c_i64,
+                                                               c_vp, c_vp, c_sz, c_vp])
+    L.mf_attention_split_workspace_bytes.restype = c_sz
+    L.mf_attention_split_workspace_bytes.argtypes = [c_int] * 8
+    L.mf_attention_window_varlen.restype = c_int
+    L.mf_attention_window_varlen.argtypes = ([c_int, c_vp, c_vp] + rows * 3 + [c_int] * 6 +
+                                             [c_vp, c_int, c_int, c_vp, c_i64, c_vp, c_vp])
+    L.mf_attention_decode_workspace_bytes.restype = c_sz
+    L.mf_attention_decode_workspace_bytes.argtypes = [c_int] * 8
+    cache = [c_vp, c_vp, c_i64, c_int, c_vp, c_int, c_vp, c_int, c_int, c_int]
+    L.mf_attention_decode.restype = c_int
+    L.mf_attention_decode.argtypes = ([c_vp, c_i64] + cache + [c_int] * 3 +
+                                      [c_vp, c_int, c_int, c_vp, c_i64, c_vp, c_vp, c_vp, c_i64,
+                                       c_vp, c_sz, c_vp])
+    L.mf_key_mass_qk_workspace_bytes.restype = c_sz
+    L.mf_key_mass_qk_workspace_bytes.argtypes = [c_int] * 8
+    L.mf_key_mass_qk.restype = c_int
+    L.mf_key_mass_qk.argtypes = (rows * 2 + [c_vp, c_vp] + [c_int] * 8 +
+                                 [c_vp, c_vp, c_vp, c_sz, c_vp])
+    L.mf_cache_evict.restype = c_int
+    L.mf_cache_evict.argtypes = ([c_vp, c_i64] + cache + [c_int] * 5 +
+                                 [c_vp, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp])
     _lib = L
     return L
 

@@ -496,6 +496,235 @@ int mf_bm_stats(mf_block_manager* m, int64_t* out);
 int mf_pool_store(const void* vals, int64_t nnzb, const int32_t* pages, void* pool,
                   int64_t n_pages, int dtype, int H_s, int B, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The attention around the reuse path.  The sender's layers and the
+ * receiver's first layers run attention as usual (paper page, "MapFlow System
+ * Design" item 1; article, second section): the calls below take projected
+ * rows to Q and K, run the attention of a prompt and of single tokens over a
+ * cache, add up how much weight every cached key received, and cut a cache to
+ * a budget by that weight.  mf_qk_norm_rope writes the Q and K that mf_row_lse
+ * and the compression calls read, and mf_attention_window's lse is theirs.
+ *
+ * Common conventions
+ *  - Element (row n, head h, dim e) of a strided tensor X lies at
+ *    X[n*ldX + h*hsX + e], strides >= 0; those of an output must keep its rows
+ *    apart.  [H][N][d] has ldX = d, hsX = N*d; [N][H][d] has ldX = H*d, hsX = d.
+ *  - A cache is a pair of pools K, V [n_pages][H_kv][page][d] of `dtype`,
+ *    16-byte aligned, `page` rows to a page.  block_table (device,
+ *    [S][max_pages] int32) names the pool pages of each sequence in order;
+ *    NULL means page s*max_pages + i (a contiguous cache has max_pages = 1
+ *    and page = its capacity).  Rows on pages outside [0, n_pages) are
+ *    skipped like masked ones.  lens (device, [S] int32) holds the cached
+ *    lengths, each clamped to [0, max_len]; max_len <= max_pages*page.
+ *  - Mask: a query at position p sees key j when j <= p and (j > p - window or
+ *    j < sinks).  window = 0 means no limit; sinks are the first tokens that
+ *    stay visible under a window.  What masked keys hold (infinities and NaN
+ *    included) does not reach any result.  A query that sees no key gets
+ *    O = 0 and lse = -infinity.
+ *  - Scores are scale[h] * (q . k) with scale (device, [H] float32) of either
+ *    sign, accumulated in fp32; the softmax's maximum, sum and lse (natural
+ *    logarithm) are fp32.  Query head h reads KV head h / (H / H_kv).
+ *  - MF_F16 / MF_BF16 run on matrix cores; the weights exp(s - max), at most 1,
+ *    are rounded to the storage type before they multiply V, with fp32
+ *    accumulation, and the output is rounded once.  MF_F32 is fp32 throughout.
+ *  - d in {64, 128}; head counts in [1, 64], H_kv dividing H.
+ * ---------------------------------------------------------------------- */
+
+typedef enum {
+  MF_ROPE_PLAIN = 0,  /* f_i = base^(-2i/rot) */
+  MF_ROPE_LINEAR = 1, /* f_i / factor: positions interpolated */
+  MF_ROPE_NTK = 2,    /* base replaced by base * factor^(rot/(rot-2)) */
+  MF_ROPE_YARN = 3    /* interpolated by parts (YaRN): see mf_rope_frequencies */
+} mf_rope_scaling;
+
+typedef enum {
+  MF_ROPE_HALF = 0,       /* pairs (i, i + rot/2) */
+  MF_ROPE_INTERLEAVED = 1 /* pairs (2i, 2i + 1) */
+} mf_rope_layout;
+
+/*
+ * Rotary frequencies f_i, i < rot/2, in radians per position (host, [rot/2]
+ * float64; the angle of a far position needs more than 32 bits), and the
+ * factor that the rotated dims are multiplied by (host; 1 except for
+ * MF_ROPE_YARN).  MF_ROPE_YARN: with D(t) = rot ln(orig_len / (2 pi t)) /
+ * (2 ln base), lo = max(floor D(beta_fast), 0), hi = min(ceil D(beta_slow),
+ * rot - 1) and r_i = clamp((i - lo) / max(hi - lo, 0.001), 0, 1), the frequency
+ * is f_i (1 - r_i + r_i / factor) and the attention factor 0.1 ln(factor) + 1.
+ * orig_len and the betas are read by MF_ROPE_YARN only.
+ *  Errors: MF_ERR_INVALID for null pointers, rot odd or outside [2, 256],
+ *  base <= 1, factor < 1, an unknown scaling, rot = 2 with MF_ROPE_NTK, or (by
+ *  parts) orig_len <= 0 or not 0 < beta_slow < beta_fast.
+ */
+int mf_rope_frequencies(int rot, double base, int scaling, double factor, double orig_len,
+                        double beta_fast, double beta_slow, double* freq, double* attn_factor);
+
+/*
+ * Per-head RMS norm and rotary positions of q and k in one pass:
+ *   y = x / sqrt(mean_e x_e^2 + eps) * w       (w NULL: y = x, no norm)
+ *   (a, b) -> (a cos t - b sin t, b cos t + a sin t) * attn_factor,
+ *   t = positions[n] * freq[i], for the pairs of the first `rot` dims.
+ * Statistics and products are fp32, angles fp64 before their reduction; each
+ * element is rounded once to `dtype`.
+ *
+ *  q, k       device, rows of H_q*d and H_k*d elements at strides ldq and ldk
+ *             (slices of a fused projection are fine).
+ *  wq, wk     device, [d] of `dtype`, or NULL.
+ *  freq       device, [rot/2] float64 (NULL when rot = 0).
+ *  positions  device, [N] int32.
+ *  Q, K       device, strided [N] x [H_q] and [N] x [H_k] rows, written.
+ *             Q may be q itself (ldQ = ldq, hsQ = d), K likewise; outputs must
+ *             not overlap inputs otherwise.
+ *  N = 0 writes nothing.  Bases and strides off 16 bytes are accepted and
+ *  read element by element.
+ *  Errors: MF_ERR_INVALID for null pointers, N < 0, bad d, head counts, dtype
+ *  or strides, rot odd or outside [0, d], an unknown layout, eps < 0 or NaN.
+ */
+int mf_qk_norm_rope(int dtype, int N, int d, const void* q, int H_q, int64_t ldq, const void* k,
+                    int H_k, int64_t ldk, const void* wq, const void* wk, float eps,
+                    const double* freq, int rot, int layout, float attn_factor,
+                    const int32_t* positions, void* Q, int64_t ldQ, int64_t hsQ, void* K,
+                    int64_t ldK, int64_t hsK, void* stream);
+
+/*
+ * The same, with k's rows written into a cache and v's copied beside them:
+ * token n goes to cache row slots[n], that is row slots[n] % page of page
+ * slots[n] / page.  Tokens whose slot lies outside [0, n_pages*page) write no
+ * cache row (their Q is written); slots inside must be distinct.
+ *  v       device, rows of H_k*d elements at stride ldv.
+ *  K, V    device pools [n_pages][H_k][page][d], 16-byte aligned.
+ *  slots   device, [N] int64.
+ *  Errors: as mf_qk_norm_rope, and MF_ERR_INVALID for n_pages < 0, page < 1 or
+ *  misaligned pools.
+ */
+int mf_qk_norm_rope_cache(int dtype, int N, int d, const void* q, int H_q, int64_t ldq,
+                          const void* k, int H_k, int64_t ldk, const void* v, int64_t ldv,
+                          const void* wq, const void* wk, float eps, const double* freq, int rot,
+                          int layout, float attn_factor, const int32_t* positions, void* Q,
+                          int64_t ldQ, int64_t hsQ, const int64_t* slots, void* K, void* V,
+                          int64_t n_pages, int page, void* stream);
+
+/*
+ * Causal attention of N_q queries at the end of N_k keys (query i sits at
+ * position N_k - N_q + i) under the mask above.
+ *  Q, K, V  device, strided: [N_q] x [H], [N_k] x [H_kv], [N_k] x [H_kv] rows.
+ *  O        device, O[i*ldO + h*d + e], ldO >= H*d; must not overlap inputs.
+ *  lse      device, [H][N_q] float32, or NULL.
+ *  workspace  device scratch, or NULL.  A workspace of at least
+ *           mf_attention_split_workspace_bytes(...) bytes (when that is not 0)
+ *           lets few queries over many keys split the keys over workgroups;
+ *           parts are joined in a fixed order.  No initialisation needed.
+ *  N_q = 0 writes nothing; with N_k = 0 every query sees no key.
+ *  Bases or strides off 16 bytes take a plain kernel.
+ *  Errors: MF_ERR_INVALID for null pointers, negative sizes, window or sinks,
+ *  bad head counts, d, dtype or strides, O equal to an input.
+ */
+int mf_attention_window(const void* Q, int64_t ldQ, int64_t hsQ, const void* K, int64_t ldK,
+                        int64_t hsK, const void* V, int64_t ldV, int64_t hsV, int dtype, int H,
+                        int H_kv, int N_q, int N_k, int d, const float* scale, int window,
+                        int sinks, void* O, int64_t ldO, float* lse, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Workspace bytes that let mf_attention_window split the keys (0: it would not). */
+size_t mf_attention_split_workspace_bytes(int dtype, int H, int H_kv, int N_q, int N_k, int d,
+                                          int window, int sinks);
+
+/*
+ * mf_attention_window over a packed batch in one launch: sequence s holds rows
+ * cu_q[s] .. cu_q[s+1]-1 of Q, O and lse and rows cu_k[s] .. cu_k[s+1]-1 of K
+ * and V, each with its own positions.
+ *  S            host, number of sequences, >= 0.
+ *  cu_q, cu_k   device, [S+1] int32, nondecreasing from 0.
+ *  N_q, N_k     host, rows of Q and K/V; they size the grid and bound every
+ *               access, whatever the tables hold.  Rows of O and lse behind the
+ *               last sequence are left as they were.
+ *  Errors: as mf_attention_window, and MF_ERR_INVALID for S < 0.
+ */
+int mf_attention_window_varlen(int S, const int32_t* cu_q, const int32_t* cu_k, const void* Q,
+                               int64_t ldQ, int64_t hsQ, const void* K, int64_t ldK, int64_t hsK,
+                               const void* V, int64_t ldV, int64_t hsV, int dtype, int H, int H_kv,
+                               int N_q, int N_k, int d, const float* scale, int window, int sinks,
+                               void* O, int64_t ldO, float* lse, void* stream);
+
+/* Workspace bytes mf_attention_decode needs: partial outputs of the parts that
+ * long caches are split into and, with_mass != 0, the scores of S*H*max_len
+ * keys. */
+size_t mf_attention_decode_workspace_bytes(int S, int max_len, int H, int H_kv, int d, int window,
+                                           int sinks, int with_mass);
+
+/*
+ * Attention of one query per sequence, at the position of its last cached row
+ * (lens[s] - 1: the token's own K and V are cached before the call), over a
+ * cache as described above; optionally the weight that every cached row
+ * received is added up:
+ *   mass_out[s][g][j] = mass_in[s][g][j] + sum_{h of group g} weight_h[j],  j < lens[s].
+ *  Q         device, Q[s*ldQ + h*d + e], ldQ >= H*d.
+ *  O         device, O[s*ldO + h*d + e], ldO >= H*d; must not overlap inputs.
+ *  lse       device, [S][H] float32, or NULL.
+ *  mass_out  device, [S][H_kv][ldmass] float32, ldmass >= max_len, or NULL;
+ *            entries from lens[s] on are left as they were.  mass_in: the same
+ *            layout, may be mass_out itself; NULL means 0.
+ *  workspace device scratch of >= mf_attention_decode_workspace_bytes bytes.
+ *  The result does not depend on timing: parts are joined in a fixed order.
+ *  Errors: MF_ERR_INVALID for null pointers, negative sizes, window or sinks,
+ *  bad head counts, d, dtype or strides, max_len > max_pages*page, misaligned
+ *  pools, mass_in without mass_out, a short workspace.
+ */
+int mf_attention_decode(const void* Q, int64_t ldQ, const void* K, const void* V, int64_t n_pages,
+                        int page, const int32_t* block_table, int max_pages, const int32_t* lens,
+                        int dtype, int S, int max_len, int H, int H_kv, int d, const float* scale,
+                        int window, int sinks, void* O, int64_t ldO, float* lse,
+                        const float* mass_in, float* mass_out, int64_t ldmass, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Workspace bytes mf_key_mass_qk needs (0 for bad sizes). */
+size_t mf_key_mass_qk_workspace_bytes(int dtype, int H, int H_kv, int N_q, int N_k, int d,
+                                      int window, int sinks);
+
+/*
+ * Accumulated weight of every key of a prompt, the per-key counterpart of
+ * mf_block_mass_qk:
+ *   mass_out[g][j] = mass_in[g][j] + sum_{h of group g} sum_i exp(s_h[i][j] - lse[h][i])
+ * over the queries i that see key j under the mask above, with the positions of
+ * mf_attention_window (N_q < N_k: the last N_q queries only).  lse (device,
+ * [H][N_q] float32) comes from mf_attention_window or mf_row_lse; queries
+ * whose lse is -infinity add nothing.
+ *  Q, K      device, strided.
+ *  mass_out  device, [H_kv][N_k] float32; mass_in may be mass_out; NULL means 0.
+ *  workspace device, >= mf_key_mass_qk_workspace_bytes bytes.
+ *  Sums run in a fixed order, at most 256 terms to an fp32 partial before fp64.
+ *  Errors: MF_ERR_INVALID for null pointers, negative sizes, window or sinks,
+ *  bad head counts, d, dtype or strides, a short workspace.
+ */
+int mf_key_mass_qk(const void* Q, int64_t ldQ, int64_t hsQ, const void* K, int64_t ldK, int64_t hsK,
+                   const float* scale, const float* lse, int dtype, int H, int H_kv, int N_q,
+                   int N_k, int d, int window, int sinks, const float* mass_in, float* mass_out,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Cuts each (sequence, KV head) of a cache to at most `budget` rows: all of
+ * them when lens[s] <= budget, else the first `sinks`, the last `recent`, and
+ * the rows of largest mass among the others (equal masses: lower row first; a
+ * NaN counts as -infinity), in ascending order.
+ *  mass      device, [S][H_kv][ldmass] float32, ldmass >= max_len.
+ *  K_out, V_out  device, [S][H_kv][cap_out][d], 16-byte aligned, cap_out >=
+ *            budget: row r < n holds kept row r; rows from n = min(lens[s],
+ *            budget) on are left as they were.  They may be the pools of a
+ *            later mf_attention_decode (page = cap_out); they must not overlap
+ *            the source pools.  Kept rows on pages outside the pool become 0.
+ *  mass_out  device, [S][H_kv][cap_out] float32, or NULL: the kept masses, 0
+ *            from n on.
+ *  kept      device, [S][H_kv][budget] int32: kept rows, -1 from n on.
+ *  lens_out  device, [S] int32, or NULL: n.
+ *  Errors: MF_ERR_INVALID for null pointers, negative sizes, budget < 1, sinks
+ *  + recent > budget, cap_out < budget, bad d, H_kv or dtype, max_len >
+ *  max_pages*page, misaligned pools, an output pool equal to a source pool.
+ */
+int mf_cache_evict(const float* mass, int64_t ldmass, const void* K, const void* V, int64_t n_pages,
+                   int page, const int32_t* block_table, int max_pages, const int32_t* lens,
+                   int dtype, int S, int max_len, int H_kv, int d, int budget, int sinks,
+                   int recent, void* K_out, void* V_out, int64_t cap_out, float* mass_out,
+                   int32_t* kept, int32_t* lens_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
