@@ -35,6 +35,7 @@ DEVICE_FLAGS = [
 # accumulation registers for every score tile.
 EXTRA_FLAGS = {
     "k_qk.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "k_attn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 
