@@ -131,15 +131,15 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(const mf::EvictArg
   }
 }
 
-// grid (row chunk, sequence * H_kv); a lane moves 16 bytes of K and of V
+// one workgroup per (sequence, KV head, row chunk); a lane moves 16 bytes of K and of V
 template <int kRowBytes>
-__global__ __launch_bounds__(256) void k_evict_gather(const mf::EvictArgs a, int es) {
+__global__ __launch_bounds__(256) void k_evict_gather(const mf::EvictArgs a, int es, int chunks) {
   constexpr int LPR = kRowBytes / 16;
   constexpr int RPB = 256 / LPR;
-  const int sg = blockIdx.y;
+  const int sg = blockIdx.x / chunks;
   const int s = sg / a.H_kv, g = sg - s * a.H_kv;
   const int n = min(cache_len(a.c, s), a.budget);
-  const int r = blockIdx.x * RPB + threadIdx.x / LPR;
+  const int r = (blockIdx.x - sg * chunks) * RPB + threadIdx.x / LPR;
   const int b = 16 * (threadIdx.x % LPR);
   if (r >= n) return;
   const int j = a.kept[(int64_t)sg * a.budget + r];
@@ -157,8 +157,8 @@ __global__ __launch_bounds__(256) void k_evict_gather(const mf::EvictArgs a, int
 template <int RB>
 void gather(const mf::EvictArgs& a, int es, int rows, hipStream_t st) {
   constexpr int RPB = 256 / (RB / 16);
-  const dim3 grid((rows + RPB - 1) / RPB, a.S * a.H_kv);
-  k_evict_gather<RB><<<grid, 256, 0, st>>>(a, es);
+  const int chunks = (rows + RPB - 1) / RPB;
+  k_evict_gather<RB><<<(unsigned)a.S * a.H_kv * chunks, 256, 0, st>>>(a, es, chunks);
 }
 
 }  // namespace
