@@ -36,6 +36,7 @@ DEVICE_FLAGS = [
 EXTRA_FLAGS = {
     "k_qk.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "k_attn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "k_key_mass.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 

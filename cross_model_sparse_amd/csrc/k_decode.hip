@@ -337,63 +337,106 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_parts(const mf::DecodeAr
 }
 
 constexpr int kMassKeys = 1024;                 // keys per workgroup of the weights
+constexpr int kMaxParts = 1024;
 
-// grid (S * (1 + key chunks), H_kv): chunk 0 joins the parts of the group's heads,
-// the others add the weights of kMassKeys rows each.
+// grid (S * (G + key chunks), H_kv): the first G workgroups of a (sequence, KV
+// head) join the parts of one head each, the others add the weights of
+// kMassKeys rows each.  A head's (max, sum) pairs are read one a thread and
+// become factors in LDS; then each wavefront adds every fourth part, and the
+// four sums are added in order.
 template <class TT, int D>
 __global__ __launch_bounds__(kThreads) void k_decode_join(const mf::DecodeArgs a, const PartGrid pg, int KT,
                                                           int chunks) {
   using S = typename TT::S;
+  constexpr int NE = D / 64;
+  __shared__ float fac[kMaxParts];
+  __shared__ float acc4[kWaves][D];
+  __shared__ float red[kWaves];
   __shared__ float lse2[64];
-  const int s = blockIdx.x / (1 + chunks), chunk = blockIdx.x - s * (1 + chunks);
-  const int g = blockIdx.y, G = a.H / a.H_kv;
+  const int G = a.H / a.H_kv, g = blockIdx.y;
+  const int s = blockIdx.x / (G + chunks), chunk = blockIdx.x - s * (G + chunks);
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int len = cache_len(a.c, s);
   const Tiles tl(a, a.c.n_pages > 0 ? len : 0, KT);
-  const int np = max(1, (tl.count * (KT) + pg.units * kUnit - 1) / (pg.units * kUnit));
+  const int per = pg.units * (kUnit / KT);
+  const int np = max(1, (tl.count + per - 1) / per);
   const int64_t at0 = (int64_t)s * pg.nparts * a.H + (int64_t)g * G;
-  if (chunk == 0) {
-    for (int e = threadIdx.x; e < G * D; e += kThreads) {
-      const int hh = e / D, dim = e - hh * D;
-      float M = -INFINITY, L = 0.f, acc = 0.f;
-      for (int p = 0; p < np; ++p) M = fmaxf(M, pg.ml[at0 + (int64_t)p * a.H + hh].x);
-      const float mu = M == -INFINITY ? 0.f : M;
-      for (int p = 0; p < np; ++p) {
-        const int64_t at = at0 + (int64_t)p * a.H + hh;
-        const float2 t = pg.ml[at];
-        const float f = __builtin_amdgcn_exp2f(t.x - mu);
-        L = fmaf(t.y, f, L);
-        acc = fmaf(pg.part[at * D + dim], f, acc);
-      }
-      const float inv = L == 0.f ? 0.f : 1.f / L;
-      const int64_t h = (int64_t)g * G + hh;
-      ((S*)a.O)[(int64_t)s * a.ldO + h * D + dim] = TT::fromf(acc * inv);
-      if (a.lse && dim == 0) a.lse[(int64_t)s * a.H + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2f;
+  auto all_max = [&](float x) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor(x, o));
+    return x;
+  };
+  auto all_sum = [&](float x) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
+    return x;
+  };
+  if (chunk < G) {
+    const int64_t at = at0 + chunk;
+    float M = -INFINITY;
+    for (int p = t; p < np; p += kThreads) {
+      fac[p] = pg.ml[at + (int64_t)p * a.H].x;
+      M = fmaxf(M, fac[p]);
     }
+    M = all_max(M);
+    if (lane == 0) red[wave] = M;
+    __syncthreads();
+    M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    const float mu = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    for (int p = t; p < np; p += kThreads) {
+      const float f = __builtin_amdgcn_exp2f(fac[p] - mu);
+      L = fmaf(pg.ml[at + (int64_t)p * a.H].y, f, L);
+      fac[p] = f;
+    }
+    L = all_sum(L);
+    __syncthreads();
+    if (lane == 0) red[wave] = L;
+    float acc[NE] = {};
+#pragma unroll 4
+    for (int p = wave; p < np; p += kWaves) {
+      const float* src = pg.part + (at + (int64_t)p * a.H) * D + NE * lane;
+      const float f = fac[p];
+#pragma unroll
+      for (int c = 0; c < NE; ++c) acc[c] = fmaf(src[c], f, acc[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < NE; ++c) acc4[wave][NE * lane + c] = acc[c];
+    __syncthreads();
+    L = ((red[0] + red[1]) + red[2]) + red[3];
+    const int64_t h = (int64_t)g * G + chunk;
+    if (t < D) {
+      const float v = ((acc4[0][t] + acc4[1][t]) + acc4[2][t]) + acc4[3][t];
+      ((S*)a.O)[(int64_t)s * a.ldO + h * D + t] = TT::fromf(L == 0.f ? 0.f : v / L);
+    }
+    if (t == 0 && a.lse) a.lse[(int64_t)s * a.H + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2f;
     return;
   }
-  const int j0 = (chunk - 1) * kMassKeys;
+  const int j0 = (chunk - G) * kMassKeys;
   if (j0 >= len) return;
-  if ((int)threadIdx.x < G) {
+  for (int hh = wave; hh < G; hh += kWaves) {
     float M = -INFINITY, L = 0.f;
-    for (int p = 0; p < np; ++p) M = fmaxf(M, pg.ml[at0 + (int64_t)p * a.H + threadIdx.x].x);
+    for (int p = lane; p < np; p += 64) M = fmaxf(M, pg.ml[at0 + (int64_t)p * a.H + hh].x);
+    M = all_max(M);
     const float mu = M == -INFINITY ? 0.f : M;
-    for (int p = 0; p < np; ++p) {
-      const float2 t = pg.ml[at0 + (int64_t)p * a.H + threadIdx.x];
-      L = fmaf(t.y, __builtin_amdgcn_exp2f(t.x - mu), L);
+    for (int p = lane; p < np; p += 64) {
+      const float2 x = pg.ml[at0 + (int64_t)p * a.H + hh];
+      L = fmaf(x.y, __builtin_amdgcn_exp2f(x.x - mu), L);
     }
+    L = all_sum(L);
     // +infinity: no key of this head is visible, every weight is 0
-    lse2[threadIdx.x] = L == 0.f ? INFINITY : M + log2f(L);
+    if (lane == 0) lse2[hh] = L == 0.f ? INFINITY : M + log2f(L);
   }
   __syncthreads();
   const float* score = pg.score + ((int64_t)s * a.H + (int64_t)g * G) * pg.slots;
   const int64_t mrow = ((int64_t)s * a.H_kv + g) * a.ldmass;
-  for (int j = j0 + threadIdx.x; j < min(j0 + kMassKeys, len); j += kThreads) {
-    const int t = j / KT;
-    const int it = t < tl.nS ? t : t - tl.tw0 + tl.nS;
+  for (int j = j0 + t; j < min(j0 + kMassKeys, len); j += kThreads) {
+    const int tile = j / KT;
+    const int it = tile < tl.nS ? tile : tile - tl.tw0 + tl.nS;
     float w = 0.f;
     if (j < tl.n && (j >= tl.w0 || j < a.sinks))
       for (int hh = 0; hh < G; ++hh) {
-        const float x = score[(int64_t)hh * pg.slots + it * KT + (j - t * KT)];
+        const float x = score[(int64_t)hh * pg.slots + it * KT + (j - tile * KT)];
         w += x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x - lse2[hh]);
       }
     a.mass_out[mrow + j] = (a.mass_in ? a.mass_in[mrow + j] : 0.f) + w;
@@ -437,7 +480,7 @@ hipError_t run(const mf::DecodeArgs& a, void* ws, hipStream_t st) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !join) return e;
   const int chunks = a.mass_out ? (a.c.max_len + kMassKeys - 1) / kMassKeys : 0;
-  k_decode_join<TT, D><<<dim3(a.S * (1 + chunks), a.H_kv), kThreads, 0, st>>>(a, pg, KT, chunks);
+  k_decode_join<TT, D><<<dim3(a.S * (a.H / a.H_kv + chunks), a.H_kv), kThreads, 0, st>>>(a, pg, KT, chunks);
   return hipGetLastError();
 }
 

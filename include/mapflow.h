@@ -691,7 +691,8 @@ size_t mf_key_mass_qk_workspace_bytes(int dtype, int H, int H_kv, int N_q, int N
  *  Q, K      device, strided.
  *  mass_out  device, [H_kv][N_k] float32; mass_in may be mass_out; NULL means 0.
  *  workspace device, >= mf_key_mass_qk_workspace_bytes bytes.
- *  Sums run in a fixed order, at most 256 terms to an fp32 partial before fp64.
+ *  Sums run in a fixed order: fp32 over 16 queries, over at most 256 of those
+ *  sums, then fp64 over runs of queries and heads.
  *  Errors: MF_ERR_INVALID for null pointers, negative sizes, window or sinks,
  *  bad head counts, d, dtype or strides, a short workspace.
  */

@@ -16,8 +16,8 @@ O          each weight enters rounded to the storage type (u) and with the relat
            final rounding u |O|.  An fp16 weight below 2^-14 is off by at most 2^-25
            instead of u of itself: n 2^-25 max|v| more.
 lse        ds + (2 n + 8) f + 2 f |lse|.
-mass       a weight from a given lse: ds + 2 f |lse| + 4 f relative, partial sums of
-           at most 256 terms: 256 f, the final rounding f.
+mass       a weight from a given lse: ds + 2 f |lse| + 4 f relative; sums of 16 terms,
+           then of at most 256 of those: 272 f; the final rounding f.
 """
 from __future__ import annotations
 
@@ -60,7 +60,7 @@ def mass_rel(r, d):
     if r["lse"].size == 0:
         return 0.0
     fin = np.abs(np.where(np.isfinite(r["lse"]), r["lse"], 0.0)).max()
-    return 2 * score_err(float(r["bound"].max()), d) + 4 * F * fin + (256 + 8) * F
+    return 2 * score_err(float(r["bound"].max()), d) + 4 * F * fin + (272 + 8) * F
 
 
 def close(got, ref, tol, what):
