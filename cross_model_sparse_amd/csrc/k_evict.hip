@@ -2,8 +2,8 @@
 //
 // k_evict_select, one workgroup per (sequence, KV head): the budget-th largest
 // mass is found digit by digit on order-preserving integer keys (four 8-bit
-// histograms over the row, which stays in L2), then the kept rows are written
-// in ascending order: each wavefront owns a contiguous run of rows, counts its
+// histograms, one copy a wavefront), then the kept rows are written in
+// ascending order: each wavefront owns a contiguous run of rows, counts its
 // rows above the threshold and at it, and after one prefix over the wavefronts
 // places its own by ballots.  Rows at the threshold are taken lowest first.
 // k_evict_gather copies the kept rows, 16 bytes a lane: every kept row is read
@@ -27,8 +27,12 @@ __device__ __forceinline__ unsigned mass_key(float f) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+// NR > 0: a thread holds its NR candidates' keys in registers, so that the row
+// is read once (rows of up to 1024 NR); NR = 0: every pass reads it again.
+template <int NR>
 __global__ __launch_bounds__(kSelThreads) void k_evict_select(const mf::EvictArgs a) {
-  __shared__ unsigned hist[kSelWaves][256];
+  __shared__ __align__(16) unsigned hist[kSelWaves][256];
+  __shared__ __align__(16) unsigned total[256];
   __shared__ unsigned above_w[kSelWaves], tie_w[kSelWaves];
   __shared__ unsigned s_digit, s_left;
   const int sg = blockIdx.x;
@@ -39,11 +43,27 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(const mf::EvictArg
   const float* mass = a.mass + (int64_t)sg * a.ldmass;
   int32_t* kept = a.kept + (int64_t)sg * a.budget;
   float* mo = a.mass_out ? a.mass_out + (int64_t)sg * a.cap_out : nullptr;
+  const int c0 = a.sinks, c1 = len - a.recent;  // candidates
+  // a wavefront's candidates are one run of rows
+  const int seg = NR > 0 ? 64 * NR : (max(c1 - c0, 0) / kSelWaves / 64 + 1) * 64;
+  const int w0 = (int)min((int64_t)c0 + (int64_t)wave * seg, (int64_t)max(c1, c0));
+  const int w1 = (int)min((int64_t)w0 + seg, (int64_t)max(c1, c0));
+  float mass_r[NR > 0 ? NR : 1];
+  const bool cut = len > a.budget;
+  if constexpr (NR > 0) {
+    if (cut) {
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        const int j = w0 + 64 * i + lane;
+        mass_r[i] = j < w1 ? mass[j] : 0.f;
+      }
+    }
+  }
   if (t == 0 && a.lens_out && sg % a.H_kv == 0) a.lens_out[s] = n;
   for (int64_t r = n + t; r < a.budget; r += kSelThreads) kept[r] = -1;
   if (mo)
     for (int64_t r = n + t; r < a.cap_out; r += kSelThreads) mo[r] = 0.f;
-  if (len <= a.budget) {
+  if (!cut) {
     for (int r = t; r < n; r += kSelThreads) {
       kept[r] = r;
       if (mo) mo[r] = mass[r];
@@ -59,53 +79,72 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(const mf::EvictArg
     kept[n - a.recent + r] = len - a.recent + r;
     if (mo) mo[n - a.recent + r] = mass[len - a.recent + r];
   }
-  const int c0 = a.sinks, c1 = len - a.recent;  // candidates
   unsigned want = n - a.sinks - a.recent;       // < c1 - c0, since len > budget
   if (want == 0) return;
+  // f(key, mass, present) for the wavefront's rows, 64 at a time
+  auto each = [&](auto&& f) {
+    if constexpr (NR > 0) {
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+        if (w0 + 64 * i < w1) f(w0 + 64 * i + lane, mass_r[i], w0 + 64 * i + lane < w1);
+    } else {
+      for (int j = w0; j < w1; j += 64) {
+        const bool in = j + lane < w1;
+        f(j + lane, in ? mass[j + lane] : 0.f, in);
+      }
+    }
+  };
 
   unsigned prefix = 0;                          // digits found so far
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = t; i < kSelWaves * 256; i += kSelThreads) (&hist[0][0])[i] = 0;
+    *reinterpret_cast<uint4*>(&hist[0][0] + 4 * t) = make_uint4(0, 0, 0, 0);
     __syncthreads();
     const unsigned hi = shift == 24 ? 0u : ~0u << (shift + 8);
-    for (int j = c0 + t; j < c1; j += kSelThreads) {
-      const unsigned k = mass_key(mass[j]);
-      if ((k & hi) == prefix) atomicAdd(&hist[wave][(k >> shift) & 255], 1u);
-    }
+    each([&](int, float m, bool in) {
+      const unsigned k = mass_key(m);
+      if (in && (k & hi) == prefix) atomicAdd(&hist[wave][(k >> shift) & 255], 1u);
+    });
     __syncthreads();
     if (t < 256) {
       unsigned v = 0;
+#pragma unroll
       for (int w = 0; w < kSelWaves; ++w) v += hist[w][t];
-      hist[0][t] = v;
+      total[t] = v;
     }
     __syncthreads();
-    if (t == 0) {
-      unsigned left = want;
-      int dgt = 255;
-      for (; dgt > 0; --dgt) {
-        const unsigned v = hist[0][dgt];
-        if (v >= left) break;
-        left -= v;
+    if (wave == 0) {
+      // lane l holds digits 4l..4l+3; `over` counts the keys of higher lanes
+      const uint4 v = *reinterpret_cast<const uint4*>(total + 4 * lane);
+      const unsigned mine = v.x + v.y + v.z + v.w;
+      unsigned incl = mine;                     // keys of this lane and higher ones
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const unsigned u = __shfl_down(incl, o);
+        incl += lane + o < 64 ? u : 0u;
       }
-      s_digit = dgt;
-      s_left = left;
+      const unsigned over = incl - mine;
+      if (over < want && want <= incl) {        // exactly one lane
+        unsigned left = want - over;
+        int dgt = 3;
+        const unsigned c[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 3; i > 0; --i)
+          if (dgt == i && c[i] < left) { left -= c[i]; dgt = i - 1; }
+        s_digit = 4 * lane + dgt;
+        s_left = left;
+      }
     }
     __syncthreads();
     prefix |= s_digit << shift;
     want = s_left;                              // still to take among this prefix
-    __syncthreads();
   }
   // keys above `prefix` are kept, and the first `want` rows equal to it
-  const int seg = (((c1 - c0) + kSelWaves - 1) / kSelWaves + 63) / 64 * 64;
-  const int64_t b0 = (int64_t)c0 + (int64_t)wave * seg;
-  const int w0 = (int)min(b0, (int64_t)c1), w1 = (int)min(b0 + seg, (int64_t)c1);
   unsigned na = 0, nt = 0;
-  for (int j = w0; j < w1; j += 64) {
-    const unsigned k = j + lane < w1 ? mass_key(mass[j + lane]) : 0u;
-    const bool in = j + lane < w1;
+  each([&](int, float m, bool in) {
+    const unsigned k = mass_key(m);
     na += __popcll(__ballot(in && k > prefix));
     nt += __popcll(__ballot(in && k == prefix));
-  }
+  });
   if (lane == 0) { above_w[wave] = na; tie_w[wave] = nt; }
   __syncthreads();
   unsigned ties = 0, out = a.sinks;
@@ -114,21 +153,19 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(const mf::EvictArg
     ties += tie_w[w];
   }
   const uint64_t below = (1ull << lane) - 1;
-  for (int j = w0; j < w1; j += 64) {
-    const bool in = j + lane < w1;
-    const float m = in ? mass[j + lane] : 0.f;
+  each([&](int j, float m, bool in) {
     const unsigned k = mass_key(m);
     const uint64_t bt = __ballot(in && k == prefix);
     const bool keep = in && (k > prefix || (k == prefix && ties + __popcll(bt & below) < want));
     const uint64_t bk = __ballot(keep);
     if (keep) {
       const unsigned o = out + __popcll(bk & below);
-      kept[o] = j + lane;
+      kept[o] = j;
       if (mo) mo[o] = m;
     }
     out += __popcll(bk);
     ties += __popcll(bt);
-  }
+  });
 }
 
 // one workgroup per (sequence, KV head, row chunk); a lane moves 16 bytes of K and of V
@@ -166,7 +203,10 @@ void gather(const mf::EvictArgs& a, int es, int rows, hipStream_t st) {
 namespace mf {
 
 hipError_t launch_evict(int dt, const EvictArgs& a, hipStream_t st) {
-  k_evict_select<<<a.S * a.H_kv, kSelThreads, 0, st>>>(a);
+  const int rows_sg = a.S * a.H_kv;
+  if (a.c.max_len <= 8 * kSelThreads) k_evict_select<8><<<rows_sg, kSelThreads, 0, st>>>(a);
+  else if (a.c.max_len <= 32 * kSelThreads) k_evict_select<32><<<rows_sg, kSelThreads, 0, st>>>(a);
+  else k_evict_select<0><<<rows_sg, kSelThreads, 0, st>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int es = dtype_bytes(dt), rows = std::min(a.budget, a.c.max_len);

@@ -449,6 +449,8 @@ EVICT = [
     ([500], 500, 8, 128, 100, 499, 4, 10),
     ([333, 40], 333, 1, 128, 16, 40, 40, 0),
     ([4100], 4100, 2, 64, 128, 1, 0, 1),
+    ([9000, 20000], 20000, 1, 64, 64, 5000, 7, 100),
+    ([40001, 300], 40001, 1, 64, 256, 9999, 3, 5),
 ]
 
 
