@@ -35,6 +35,9 @@ def _bad(msg: str):
 
 
 
+_NULL = contextlib.nullcontext()
+
+
 def _on(dev: torch.device, stream):
     """(context, handle): the stream that the call runs on, and a context in
     which allocations belong to it."""
@@ -44,23 +47,18 @@ def _on(dev: torch.device, stream):
         if stream.device != dev:
             _bad(f"stream of {stream.device}, tensors on {dev}")
         return torch.cuda.stream(stream), stream.cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        return _NULL, torch.cuda.current_stream(dev).cuda_stream
-    return torch.cuda.device(dev), torch.cuda.current_stream(dev).cuda_stream
+    handle = torch._C._cuda_getCurrentRawStream(dev.index)
+    return (_NULL if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)), handle
 
 
-_NULL = contextlib.nullcontext()
-
-
-def _same(dev: torch.device, dtype, **ts):
-    """Every given tensor lives on `dev` and (dtype not None) holds `dtype`."""
-    for name, t in ts.items():
-        if t is None:
-            continue
-        if t.device != dev:
-            _bad(f"{name} is on {t.device}, not {dev}")
-        if dtype is not None and t.dtype != dtype:
-            _bad(f"{name} must be {dtype} (got {t.dtype})")
+def _same(where: int, dtype, t: torch.Tensor | None, name: str) -> None:
+    """t (if given) lives on the device `where` (-1: the host) and holds `dtype`."""
+    if t is None:
+        return
+    if t.get_device() != where:
+        _bad(f"{name} is on {t.device}, other tensors elsewhere")
+    if dtype is not None and t.dtype is not dtype:
+        _bad(f"{name} must be {dtype} (got {t.dtype})")
 
 
 def _code(t: torch.Tensor) -> int:
@@ -70,19 +68,12 @@ def _code(t: torch.Tensor) -> int:
     return c
 
 
-def _vec(t: torch.Tensor | None, name: str, n: int, dtype, dev) -> None:
+def _full(t: torch.Tensor | None, name: str, shape: tuple, dtype, where: int) -> None:
+    """t (if given) is a contiguous tensor of that shape, type and device."""
     if t is None:
         return
-    _same(dev, dtype, **{name: t})
-    if t.dim() != 1 or t.shape[0] != n or not (t.is_contiguous() or n == 0):
-        _bad(f"{name} must be a contiguous [{n}] tensor")
-
-
-def _full(t: torch.Tensor | None, name: str, shape: tuple, dtype, dev) -> None:
-    if t is None:
-        return
-    _same(dev, dtype, **{name: t})
-    if tuple(t.shape) != shape or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != where or not t.is_contiguous():
+        _same(where, dtype, t, name)
         _bad(f"{name} must be a contiguous {list(shape)} tensor")
 
 
@@ -102,7 +93,7 @@ def _bytes_of(t: torch.Tensor | None) -> int:
 def _workspace(t, need: int, dev):
     """The caller's workspace, or a fresh one (None when none is needed)."""
     if t is not None:
-        _same(dev, None, workspace=t)
+        _same(dev.index if dev.type == "cuda" else -1, None, t, "workspace")
         if not t.is_contiguous():
             _bad("workspace must be contiguous")
         return t
@@ -145,28 +136,30 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, freq: torch.Tensor | None,
     _rows3(k, "k")
     N, H_q, d = q.shape
     H_k = k.shape[1]
-    dev, dt = q.device, q.dtype
+    dev, dt, where = q.device, q.dtype, q.get_device()
     code = _code(q)
     if k.shape[0] != N or k.shape[2] != d:
         _bad("k must match q in N and d")
     if layout not in _LAYOUT:
         _bad(f"unknown layout {layout!r}")
-    _same(dev, dt, k=k, wq=wq, wk=wk, Q=Q, K=K, v=v, V=V)
     for t, name, H in ((q, "q", H_q), (k, "k", H_k), (v, "v", H_k)):
         if t is None:
             continue
-        if t.dim() != 3 or tuple(t.shape) != (N, H, d):
+        _same(where, dt, t, name)
+        if t.shape != (N, H, d):
             _bad(f"{name} must be [{N}][{H}][{d}]")
         if N and ((H > 1 and t.stride(1) != d) or t.stride(2) != 1):
             _bad(f"{name}'s heads must lie side by side")
+    _same(where, dt, Q, "Q")
+    _same(where, dt, K, "K")
     rot = 0 if freq is None else 2 * freq.shape[0]
     if rot:
-        _vec(freq, "freq", rot // 2, torch.float64, dev)
+        _full(freq, "freq", (rot // 2,), torch.float64, where)
         if positions is None:
             _bad("positions missing")
-        _vec(positions, "positions", N, torch.int32, dev)
-    _vec(wq, "wq", d, dt, dev)
-    _vec(wk, "wk", d, dt, dev)
+        _full(positions, "positions", (N,), torch.int32, where)
+    _full(wq, "wq", (d,), dt, where)
+    _full(wk, "wk", (d,), dt, where)
     ctx, handle = _on(dev, stream)
 
     def lead(t):                                 # stride from row to row
@@ -176,7 +169,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, freq: torch.Tensor | None,
         shape = (N, H, d) if token_major else (H, N, d)
         if t is None:
             t = torch.empty(shape, dtype=dt, device=dev)
-        elif tuple(t.shape) != shape or t.stride(2) != 1:
+        elif t.shape != shape or (t.numel() and t.stride(2) != 1):
             _bad(f"{name} must be {list(shape)} with contiguous rows")
         n, h = (0, 1) if token_major else (1, 0)
         return t, (t.stride(n) if N > 1 else H * d), (t.stride(h) if H > 1 else d)
@@ -194,10 +187,10 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, freq: torch.Tensor | None,
             return Q, K
         if v is None or K is None or V is None:
             _bad("slots need v and the pools K and V")
-        _vec(slots, "slots", N, torch.int64, dev)
+        _full(slots, "slots", (N,), torch.int64, where)
         if K.dim() != 4 or K.shape[1] != H_k or K.shape[3] != d or not K.is_contiguous():
             _bad("K must be a contiguous [n_pages][H_k][page][d] pool")
-        _full(V, "V", tuple(K.shape), dt, dev)
+        _full(V, "V", K.shape, dt, where)
         _check(load().mf_qk_norm_rope_cache(*head, _p(v), lead(v), *norm, _p(slots), _p(K), _p(V),
                                             K.shape[0], K.shape[2], handle))
         return Q, K, V
@@ -216,10 +209,12 @@ def _attn_shapes(Q, K, V, scale):
     _rows3(V, "V")
     H, N_q, d = Q.shape
     H_kv, N_k, dk = K.shape
-    if dk != d or tuple(V.shape) != (N_k, H_kv, d):
+    if dk != d or V.shape != (N_k, H_kv, d):
         _bad("K must be [H_kv][N_k][d] and V [N_k][H_kv][d]")
-    _same(Q.device, Q.dtype, K=K, V=V)
-    _vec(scale, "scale", H, torch.float32, Q.device)
+    where = Q.get_device()
+    _same(where, Q.dtype, K, "K")
+    _same(where, Q.dtype, V, "V")
+    _full(scale, "scale", (H,), torch.float32, where)
     rows = (_p(Q), Q.stride(1), Q.stride(0), _p(K), K.stride(1), K.stride(0), _p(V), V.stride(0),
             V.stride(1))
     return rows, H, H_kv, N_q, N_k, d
@@ -230,14 +225,14 @@ def _attn_out(Q, H, N_q, d, out, lse):
     if out is None:
         out = torch.empty(N_q, H, d, dtype=Q.dtype, device=dev)
     else:
-        _same(dev, Q.dtype, out=out)
-        if tuple(out.shape) != (N_q, H, d) or (N_q and (out.stride(2) != 1 or
+        _same(Q.get_device(), Q.dtype, out, "out")
+        if out.shape != (N_q, H, d) or (N_q and (out.stride(2) != 1 or
                                                         (H > 1 and out.stride(1) != d))):
             _bad("out must be [N_q][H][d] with contiguous rows")
     if lse is None:
         lse = torch.empty(H, N_q, dtype=torch.float32, device=dev)
     else:
-        _full(lse, "lse", (H, N_q), torch.float32, dev)
+        _full(lse, "lse", (H, N_q), torch.float32, Q.get_device())
     return out, lse, (out.stride(0) if N_q > 1 else H * d)
 
 
@@ -277,8 +272,8 @@ def attention_window_varlen(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
     S = cu_q.shape[0] - 1 if cu_q.dim() == 1 else -1
     if S < 0:
         _bad("cu_q must be an int32 [S+1] tensor")
-    _vec(cu_q, "cu_q", S + 1, torch.int32, Q.device)
-    _vec(cu_k, "cu_k", S + 1, torch.int32, Q.device)
+    _full(cu_q, "cu_q", (S + 1,), torch.int32, Q.get_device())
+    _full(cu_k, "cu_k", (S + 1,), torch.int32, Q.get_device())
     ctx, handle = _on(Q.device, stream)
     with ctx:
         out, lse, ldO = _attn_out(Q, H, N_q, d, out, lse)
@@ -291,12 +286,12 @@ def attention_window_varlen(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
 def _cache(K, V, lens, block_table, S, max_len):
     if K.dim() != 4 or not K.is_contiguous():
         _bad("K must be a contiguous [n_pages][H_kv][page][d] pool")
-    dev = K.device
-    _full(V, "V", tuple(K.shape), K.dtype, dev)
+    where = K.get_device()
+    _full(V, "V", K.shape, K.dtype, where)
     n_pages, H_kv, page, d = K.shape
-    _vec(lens, "lens", S, torch.int32, dev)
+    _full(lens, "lens", (S,), torch.int32, where)
     if block_table is not None:
-        _same(dev, torch.int32, block_table=block_table)
+        _same(where, torch.int32, block_table, "block_table")
         if block_table.dim() != 2 or block_table.shape[0] != S or not block_table.is_contiguous():
             _bad(f"block_table must be a contiguous [{S}][max_pages] tensor")
         max_pages = block_table.shape[1]
@@ -329,9 +324,9 @@ def attention_decode(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, lens: to
     _rows3(Q, "Q")
     S, H, d = Q.shape
     cache, H_kv, dk = _cache(K, V, lens, block_table, S, max_len)
-    dev = K.device
-    _same(dev, K.dtype, Q=Q)
-    _vec(scale, "scale", H, torch.float32, dev)
+    dev, where = K.device, K.get_device()
+    _same(where, K.dtype, Q, "Q")
+    _full(scale, "scale", (H,), torch.float32, where)
     if dk != d or (S and H > 1 and Q.stride(1) != d):
         _bad("Q must be [S][H][d] with its heads side by side, d as in the cache")
     ldmass = 0
@@ -339,8 +334,8 @@ def attention_decode(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, lens: to
         if mass_out.dim() != 3:
             _bad("mass_out must be [S][H_kv][>= max_len]")
         ldmass = mass_out.shape[2]
-        _full(mass_out, "mass_out", (S, H_kv, ldmass), torch.float32, dev)
-        _full(mass_in, "mass_in", (S, H_kv, ldmass), torch.float32, dev)
+        _full(mass_out, "mass_out", (S, H_kv, ldmass), torch.float32, where)
+        _full(mass_in, "mass_in", (S, H_kv, ldmass), torch.float32, where)
     elif mass_in is not None:
         _bad("mass_in without mass_out")
     ctx, handle = _on(dev, stream)
@@ -348,14 +343,14 @@ def attention_decode(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, lens: to
         if out is None:
             out = torch.empty(S, H, d, dtype=Q.dtype, device=dev)
         else:
-            _same(dev, Q.dtype, out=out)
-            if tuple(out.shape) != (S, H, d) or (S and (out.stride(2) != 1 or
+            _same(where, Q.dtype, out, "out")
+            if out.shape != (S, H, d) or (S and (out.stride(2) != 1 or
                                                         (H > 1 and out.stride(1) != d))):
                 _bad("out must be [S][H][d] with contiguous rows")
         if lse is None:
             lse = torch.empty(S, H, dtype=torch.float32, device=dev)
         else:
-            _full(lse, "lse", (S, H), torch.float32, dev)
+            _full(lse, "lse", (S, H), torch.float32, where)
         L = load()
         need = 0 if workspace is not None else L.mf_attention_decode_workspace_bytes(
             S, int(max_len), H, H_kv, d, window, sinks, int(mass_out is not None))
@@ -384,20 +379,20 @@ def key_mass_qk(Q: torch.Tensor, K: torch.Tensor, scale: torch.Tensor, lse: torc
     _rows3(K, "K")
     H, N_q, d = Q.shape
     H_kv, N_k, dk = K.shape
-    dev = Q.device
+    dev, where = Q.device, Q.get_device()
     code = _code(Q)
     if dk != d:
         _bad("K must match Q in d")
-    _same(dev, Q.dtype, K=K)
-    _vec(scale, "scale", H, torch.float32, dev)
-    _full(lse, "lse", (H, N_q), torch.float32, dev)
-    _full(mass_in, "mass_in", (H_kv, N_k), torch.float32, dev)
+    _same(where, Q.dtype, K, "K")
+    _full(scale, "scale", (H,), torch.float32, where)
+    _full(lse, "lse", (H, N_q), torch.float32, where)
+    _full(mass_in, "mass_in", (H_kv, N_k), torch.float32, where)
     ctx, handle = _on(dev, stream)
     with ctx:
         if out is None:
             out = torch.empty(H_kv, N_k, dtype=torch.float32, device=dev)
         else:
-            _full(out, "out", (H_kv, N_k), torch.float32, dev)
+            _full(out, "out", (H_kv, N_k), torch.float32, where)
         L = load()
         need = 0 if workspace is not None else L.mf_key_mass_qk_workspace_bytes(
             code, H, H_kv, N_q, N_k, d, window, sinks)
@@ -426,14 +421,14 @@ def cache_evict(mass: torch.Tensor, K: torch.Tensor, V: torch.Tensor, lens: torc
     if max_len is None:
         max_len = ldmass
     cache, H_kv, d = _cache(K, V, lens, block_table, S, max_len)
-    dev = K.device
-    _full(mass, "mass", (S, H_kv, ldmass), torch.float32, dev)
+    dev, where = K.device, K.get_device()
+    _full(mass, "mass", (S, H_kv, ldmass), torch.float32, where)
     budget = int(budget)
     given = [t for t in (K_out, V_out, mass_out) if t is not None]
     cap = given[0].shape[2] if given and given[0].dim() >= 3 else budget
-    _full(K_out, "K_out", (S, H_kv, cap, d), K.dtype, dev)
-    _full(V_out, "V_out", (S, H_kv, cap, d), K.dtype, dev)
-    _full(mass_out, "mass_out", (S, H_kv, cap), torch.float32, dev)
+    _full(K_out, "K_out", (S, H_kv, cap, d), K.dtype, where)
+    _full(V_out, "V_out", (S, H_kv, cap, d), K.dtype, where)
+    _full(mass_out, "mass_out", (S, H_kv, cap), torch.float32, where)
     if budget < 1:
         _bad(f"budget must be >= 1 (got {budget})")
     ctx, handle = _on(dev, stream)

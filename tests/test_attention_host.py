@@ -228,7 +228,8 @@ def decode(L, **kw):
     (dict(lens=None), "lens"), (dict(K=None), "pool"), (dict(K=2 * FAKE + 8), "16-byte"), (dict(ldQ=1000), "ldQ"),
     (dict(ldO=1000), "ldO"), (dict(mi=FAKE), "mass_in"), (dict(mo=FAKE, ldm=63), "ldmass"), (dict(Q=None), "null"),
     (dict(O=None), "null"), (dict(scale=None), "null"), (dict(O=2 * FAKE), "one of the inputs"),
-    (dict(ws=None), "workspace"), (dict(wsb=0), "workspace"), (dict(ws=FAKE + 8), "16 bytes")])
+    (dict(mo=FAKE, ldm=64, ws=None), "workspace"), (dict(mo=FAKE, ldm=64, wsb=0), "workspace"),
+    (dict(ws=FAKE + 8), "16 bytes")])
 def test_decode_refusals(L, kw, frag):
     assert decode(L, **kw) == INV
     assert frag in last(L)
