@@ -23,6 +23,7 @@
 #include "mf_attn.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace {
 
@@ -48,41 +49,20 @@ __device__ __forceinline__ SeqRows seq_rows(const mf::AttnArgs& a, int s) {
   return r;
 }
 
+// One (query, head) by one wavefront over chunks of 64 keys: one key a lane for
+// the scores, D / 64 dims a lane for the output, masked keys never multiplied.
 template <class TT, int D>
-__global__ __launch_bounds__(256) void k_attn_plain(const mf::AttnArgs a) {
+struct PlainRow {
+  static constexpr int ND = D / 64;
   using S = typename TT::S;
-  constexpr int ND = D / 64;
-  const int lane = threadIdx.x & 63;
-  const int i = blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int h = blockIdx.y, g = h / (a.H / a.H_kv);
-  if (i >= a.N_q) return;
-  SeqRows r{0, a.N_q, 0, a.N_k};
-  if (a.cu_q) {
-    // last sequence that starts at or before row i
-    int lo = 0, hi = a.S;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (a.cu_q[mid + 1] <= i) lo = mid + 1; else hi = mid;
-    }
-    if (lo >= a.S) return;                      // behind the last sequence
-    r = seq_rows(a, lo);
-    if (i < r.q0 || i >= r.q1) return;
-  }
-  const int n_k = r.k1 - r.k0;
-  const int p = n_k - (r.q1 - r.q0) + (i - r.q0);
-  const S* q = (const S*)a.Q.p + (int64_t)i * a.Q.ld + (int64_t)h * a.Q.hs;
-  const S* K = (const S*)a.K.p + (int64_t)r.k0 * a.K.ld + (int64_t)g * a.K.hs;
-  const S* V = (const S*)a.V.p + (int64_t)r.k0 * a.V.ld + (int64_t)g * a.V.hs;
-  const float sc = a.scale[h] * kLog2E;
-  const int w0 = a.window > 0 ? max(0, p - a.window + 1) : 0;
   float m = -INFINITY, l = 0.f, acc[ND] = {};
-  for (int j0 = 0; j0 <= p; j0 += 64) {
-    if (j0 >= a.sinks && j0 + 63 < w0) { j0 = (w0 & ~63) - 64; continue; }
-    const int j = j0 + lane;
-    const bool vis = j <= p && (j >= w0 || j < a.sinks);
+
+  __device__ __forceinline__ void chunk(const S* q, const S* K, int64_t ldK, const S* V, int64_t ldV,
+                                        float sc, int j0, bool vis) {
+    const int lane = threadIdx.x & 63;
     float x = -INFINITY;
     if (vis) {
-      const S* k = K + (int64_t)j * a.K.ld;
+      const S* k = K + (int64_t)(j0 + lane) * ldK;
       float dot = 0.f;
       for (int e = 0; e < D; ++e) dot = fmaf(TT::tof(q[e]), TT::tof(k[e]), dot);
       x = dot * sc;
@@ -91,8 +71,7 @@ __global__ __launch_bounds__(256) void k_attn_plain(const mf::AttnArgs a) {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
     mx = fmaxf(mx, m);
-    const bool any_nan = __any(x != x);
-    if (mx == -INFINITY && !any_nan) continue;
+    if (mx == -INFINITY && !__any(x != x)) return;
     const float f = exp2f(m - mx);
     const float e = vis ? exp2f(x - mx) : 0.f;
     float t = e;
@@ -107,17 +86,54 @@ __global__ __launch_bounds__(256) void k_attn_plain(const mf::AttnArgs a) {
       const int kk = __ffsll((unsigned long long)seen) - 1;
       seen &= seen - 1;
       const float pk = __shfl(e, kk);
-      const S* v = V + (int64_t)(j0 + kk) * a.V.ld;
+      const S* v = V + (int64_t)(j0 + kk) * ldV;
 #pragma unroll
       for (int c = 0; c < ND; ++c) acc[c] = fmaf(pk, TT::tof(v[lane + 64 * c]), acc[c]);
     }
   }
-  const bool empty = l == 0.f;
-  S* o = (S*)a.O + (int64_t)i * a.ldO + (int64_t)h * D;
+  __device__ __forceinline__ void finish(const mf::AttnArgs& a, int64_t i, int h) const {
+    const int lane = threadIdx.x & 63;
+    const bool empty = l == 0.f;
+    S* o = (S*)a.O + i * a.ldO + (int64_t)h * D;
 #pragma unroll
-  for (int c = 0; c < ND; ++c) o[lane + 64 * c] = TT::fromf(empty ? 0.f : acc[c] / l);
-  if (a.lse && lane == 0)
-    a.lse[(int64_t)h * a.N_q + i] = empty ? -INFINITY : (m + log2f(l)) * kLn2f;
+    for (int c = 0; c < ND; ++c) o[lane + 64 * c] = TT::fromf(empty ? 0.f : acc[c] / l);
+    if (a.lse && lane == 0)
+      a.lse[(int64_t)h * a.N_q + i] = empty ? -INFINITY : (m + log2f(l)) * kLn2f;
+  }
+};
+
+template <class TT, int D>
+__global__ __launch_bounds__(256) void k_attn_plain(const mf::AttnArgs a) {
+  using S = typename TT::S;
+  const int lane = threadIdx.x & 63;
+  const int i = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int h = blockIdx.y, g = h / (a.H / a.H_kv);
+  if (i >= a.N_q) return;
+  SeqRows r{0, a.N_q, 0, a.N_k};
+  if (a.cu_q) {
+    // first sequence that ends behind row i
+    int lo = 0, hi = a.S;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (a.cu_q[mid + 1] <= i) lo = mid + 1; else hi = mid;
+    }
+    if (lo >= a.S) return;                      // behind the last sequence
+    r = seq_rows(a, lo);
+    if (i < r.q0 || i >= r.q1) return;
+  }
+  const int p = r.k1 - r.k0 - (r.q1 - r.q0) + (i - r.q0);
+  const S* q = (const S*)a.Q.p + (int64_t)i * a.Q.ld + (int64_t)h * a.Q.hs;
+  const S* K = (const S*)a.K.p + (int64_t)r.k0 * a.K.ld + (int64_t)g * a.K.hs;
+  const S* V = (const S*)a.V.p + (int64_t)r.k0 * a.V.ld + (int64_t)g * a.V.hs;
+  const float sc = a.scale[h] * kLog2E;
+  const int w0 = a.window > 0 ? max(0, p - a.window + 1) : 0;
+  PlainRow<TT, D> row;
+  for (int j0 = 0; j0 <= p; j0 += 64) {
+    if (j0 >= a.sinks && j0 + 63 < w0) { j0 = (w0 & ~63) - 64; continue; }
+    const int j = j0 + lane;
+    row.chunk(q, K, a.K.ld, V, a.V.ld, sc, j0, j <= p && (j >= w0 || j < a.sinks));
+  }
+  row.finish(a, i, h);
 }
 
 // ---- tiles on matrix cores -------------------------------------------------
@@ -167,25 +183,74 @@ __device__ __forceinline__ unsigned nonfinite_bits(unsigned w) {
   return ((w & Elem<TT>::kExp) + Elem<TT>::kLow) & (sizeof(typename TT::S) == 4 ? 0x80000000u : 0x80008000u);
 }
 
-// Byte offset of 16-byte piece c of row r in a K tile: the 16 lanes of a
-// b128 read take one piece of 16 consecutive rows.
+// 16-byte piece c of row r lies at place c ^ swizzle(r) of its row.  In a K
+// tile the 16 lanes of a b128 read take one piece of 16 consecutive rows; in a
+// V tile a transposing read takes 64 bytes of four consecutive rows: either way
+// the swizzle spreads them over all 64 banks.
 template <int RB>
-__device__ __forceinline__ int k_piece(int r, int c) {
-  if constexpr (RB == 128) return r * RB + 16 * (c ^ ((r >> 1) & 7));
-  else return r * RB + 16 * (c ^ (r & 15));
-}
-// The same in a V tile: a transposing read takes 64 bytes of four consecutive
-// rows, which the swizzle spreads over all 64 banks.
+__device__ __forceinline__ constexpr int k_swizzle(int r) { return RB == 128 ? (r >> 1) & 7 : r & 15; }
 template <int RB>
-__device__ __forceinline__ int v_piece(int r, int c) {
-  if constexpr (RB == 128) return r * RB + 16 * (c ^ (4 * ((r >> 1) & 1)));
-  else return r * RB + 16 * (c ^ (4 * (r & 3)));
-}
+__device__ __forceinline__ constexpr int v_swizzle(int r) { return RB == 128 ? 4 * ((r >> 1) & 1) : 4 * (r & 3); }
+template <int RB>
+__device__ __forceinline__ int k_piece(int r, int c) { return r * RB + 16 * (c ^ k_swizzle<RB>(r)); }
+template <int RB>
+__device__ __forceinline__ int v_piece(int r, int c) { return r * RB + 16 * (c ^ v_swizzle<RB>(r)); }
 
 __device__ __forceinline__ float other_half(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
 }
+
+// 16 bytes a lane from memory (uniform base, 32-bit offset a lane) into LDS at
+// lds + 16 * lane, in flight until wait_copies.  The wait states cover a base
+// in registers that a vector instruction wrote, and the copy's read of M0.
+__device__ __forceinline__ void copy16(unsigned voff, const void* base, unsigned lds) {
+  asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :: "s"(lds), "v"(voff), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ const char* uniform(const char* p) {
+  const unsigned long long v = reinterpret_cast<unsigned long long>(p);
+  const unsigned lo = __builtin_amdgcn_readfirstlane((unsigned)v);
+  const unsigned hi = __builtin_amdgcn_readfirstlane((unsigned)(v >> 32));
+  return reinterpret_cast<const char*>(((unsigned long long)hi << 32) | lo);
+}
+__device__ __forceinline__ unsigned lds_addr(const void* p) {
+  return (unsigned)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
+// The rare case of a workgroup whose partly masked tiles hold infinities or NaN
+// in V: its rows again, key by key over the same tiles, one wavefront's 32 rows
+// from r0 in turn.
+template <class TT, int D>
+__device__ void redo_rows(const mf::AttnArgs& a, const TileGrid& tg, const SeqRows& sr, int r0, int off,
+                          int h, int split, int it0, int it1, int nS, int tw0, int KT) {
+  using S = typename TT::S;
+  const int lane = threadIdx.x & 63, g = h / (a.H / a.H_kv);
+  const S* K = (const S*)a.K.p + (int64_t)sr.k0 * a.K.ld + (int64_t)g * a.K.hs;
+  const S* V = (const S*)a.V.p + (int64_t)sr.k0 * a.V.ld + (int64_t)g * a.V.hs;
+  const float sc = a.scale[h] * kLog2E;
+  for (int r = r0; r < min(r0 + 32, sr.q1 - sr.q0); ++r) {
+    const int64_t i = sr.q0 + r;
+    const int p = off + r, w0 = a.window > 0 ? max(0, p - a.window + 1) : 0;
+    const S* q = (const S*)a.Q.p + i * a.Q.ld + (int64_t)h * a.Q.hs;
+    PlainRow<TT, D> row;
+    for (int it = it0; it < it1; ++it) {
+      const int j0 = (it < nS ? it : tw0 + it - nS) * KT, j = j0 + lane;
+      row.chunk(q, K, a.K.ld, V, a.V.ld, sc, j0, lane < KT && j <= p && (j >= w0 || j < a.sinks));
+    }
+    if (tg.nsplit > 1) {
+      const int64_t at = ((int64_t)split * a.H + h) * a.N_q + i;
+      if (lane == 0) tg.ml[at] = make_float2(row.m, row.l);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) tg.part[at * D + lane + 64 * c] = row.acc[c];
+    } else {
+      row.finish(a, i, h);
+    }
+  }
+}
+
+#define PIN() __builtin_amdgcn_sched_barrier(0)
 
 template <class TT, int D>
 __global__ __launch_bounds__(kThreads, 2) void k_attn_tiles(const mf::AttnArgs a, const TileGrid tg) {
@@ -196,13 +261,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_tiles(const mf::AttnArgs a
   constexpr int NB = KT / 32;                   // 32-key score blocks per tile
   constexpr int RB = D * (int)sizeof(S);        // bytes per row
   constexpr int CH = RB / 16;                   // 16-byte pieces per row
-  constexpr int NP = KT * CH / kThreads;        // pieces of a tile per thread
-  constexpr int RSTEP = kThreads / CH;          // rows between a thread's pieces
   constexpr int NQ = RB / 32;                   // 16-byte query pieces per lane
   constexpr int ND = D / 32;                    // 32-dim output blocks
   constexpr int kTile = KT * RB;
-  __shared__ __align__(16) unsigned char smem[4 * kTile];   // K0 V0 K1 V1
-  __shared__ int bad[2];                        // tile (number + 1) whose V holds a non-finite value
+  constexpr int NC = kTile / 4 / 1024;          // copies of a wavefront per tile
+  constexpr int CR = 1024 / RB;                 // rows per copy
+  __shared__ __align__(16) unsigned char smem[4 * kTile];   // K0 K1 V0 V1
+  __shared__ int redo;                          // a partly masked tile's V is not finite
 
   const int lane = threadIdx.x & 63, hf = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -258,7 +323,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_tiles(const mf::AttnArgs a
   u32x4 q[NQ];
   {
     const int rr = sr.q0 + min(row, n_q - 1);
-    const char* qp = (const char*)a.Q.p + ((int64_t)rr * a.Q.ld + (int64_t)h * a.Q.hs) * sizeof(S) + 16 * hf;
+    const char* qp = (const char*)a.Q.p + ((int64_t)rr * a.Q.ld + (int64_t)h * a.Q.hs) * (int64_t)sizeof(S) + 16 * hf;
     const unsigned flip = sc < 0.f ? (k16 ? 0x80008000u : 0x80000000u) : 0u;
 #pragma unroll
     for (int s = 0; s < NQ; ++s) {
@@ -267,48 +332,34 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_tiles(const mf::AttnArgs a
     }
   }
 
-  // thread's pieces of a tile: rows tr, tr + RSTEP, ..., piece tc
-  const int tr = threadIdx.x / CH, tc = threadIdx.x % CH;
-  const char* Kg = (const char*)a.K.p + ((int64_t)sr.k0 * a.K.ld + (int64_t)g * a.K.hs) * sizeof(S);
-  const char* Vg = (const char*)a.V.p + ((int64_t)sr.k0 * a.V.ld + (int64_t)g * a.V.hs) * sizeof(S);
+  // Copies: wavefront w fetches rows (KT/4) w .. of a tile, CR rows at a time;
+  // lane l lands at byte 16 l, which holds the piece that the swizzle puts there.
   const int64_t ldK = a.K.ld * (int64_t)sizeof(S), ldV = a.V.ld * (int64_t)sizeof(S);
-  const unsigned ko = (unsigned)(tr * ldK) + 16 * tc, vo = (unsigned)(tr * ldV) + 16 * tc;
-  u32x4 ks[NP], vs[NP];
-  auto load = [&](int it) {
-    const int j0 = key0(it);
-    if (j0 + KT <= n_k) {
+  const char* Kg = (const char*)a.K.p + ((int64_t)sr.k0 * a.K.ld + (int64_t)g * a.K.hs) * (int64_t)sizeof(S);
+  const char* Vg = (const char*)a.V.p + ((int64_t)sr.k0 * a.V.ld + (int64_t)g * a.V.hs) * (int64_t)sizeof(S);
+  const int cr = lane / CH, cp = lane % CH;     // row within a copy, place within the row
+  // The swizzles are linear in the bits of the row, and a lane's row within a
+  // copy and the copy's first row have no bit in common.
+  const unsigned kx = 16 * (cp ^ k_swizzle<RB>(cr)), vx = 16 * (cp ^ v_swizzle<RB>(cr));
+  const unsigned kr = (unsigned)(cr * ldK), vr = (unsigned)(cr * ldV);
+  const unsigned lds0 = lds_addr(smem) + wave * (kTile / 4);
+  auto copy = [&](int it, int buf, auto isv) {
+    constexpr bool kV = decltype(isv)::value;
+    const int j0 = key0(it) + wave * (KT / 4);
+    const unsigned dst = lds0 + buf * kTile;
+    const char* b = uniform(kV ? Vg : Kg);
+    const int64_t ld = kV ? ldV : ldK;
 #pragma unroll
-      for (int n = 0; n < NP; ++n) {
-        ks[n] = *reinterpret_cast<const u32x4*>(Kg + (j0 + n * RSTEP) * ldK + ko);
-        vs[n] = *reinterpret_cast<const u32x4*>(Vg + (j0 + n * RSTEP) * ldV + vo);
+    for (int n = 0; n < NC; ++n) {
+      const int r = wave * (KT / 4) + CR * n;   // the copy's first row within the tile
+      const unsigned x = kV ? vx ^ (16 * v_swizzle<RB>(r)) : kx ^ (16 * k_swizzle<RB>(r));
+      const int j = j0 + CR * n;
+      if (j + CR <= n_k) {
+        copy16(x + (kV ? vr : kr), b + j * ld, dst + 1024 * n);
+      } else {                                  // rows behind the last key repeat it
+        const int jf = min(j, n_k - 1);
+        copy16(x + (unsigned)((min(j + cr, n_k - 1) - jf) * ld), b + jf * ld, dst + 1024 * n);
       }
-    } else {                                    // rows behind the last key: a valid K row, V = 0
-#pragma unroll
-      for (int n = 0; n < NP; ++n) {
-        const int j = j0 + tr + n * RSTEP;
-        const int64_t jj = min(j, n_k - 1);
-        ks[n] = *reinterpret_cast<const u32x4*>(Kg + jj * ldK + 16 * tc);
-        vs[n] = *reinterpret_cast<const u32x4*>(Vg + jj * ldV + 16 * tc);
-        if (j >= n_k) vs[n] = u32x4{0, 0, 0, 0};
-      }
-    }
-  };
-  auto store = [&](int it) {
-    unsigned char* kb = smem + (it & 1) * 2 * kTile;
-#pragma unroll
-    for (int n = 0; n < NP; ++n) {
-      *reinterpret_cast<u32x4*>(kb + k_piece<RB>(tr + n * RSTEP, tc)) = ks[n];
-      *reinterpret_cast<u32x4*>(kb + kTile + v_piece<RB>(tr + n * RSTEP, tc)) = vs[n];
-    }
-    // a masked key's weight is 0, but 0 * inf is not: note tiles that need care
-    const int j0 = key0(it), j1 = j0 + KT - 1;
-    if (!(j1 <= Pa && (!win || j0 > Pb - a.window || j1 < a.sinks))) {
-      unsigned f = 0;
-#pragma unroll
-      for (int n = 0; n < NP; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f |= nonfinite_bits<TT>(vs[n][i]);
-      if (f) bad[it & 1] = it + 1;
     }
   };
 
@@ -317,143 +368,219 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_tiles(const mf::AttnArgs a
   for (int b = 0; b < ND; ++b) o[b] = f32x16{};
   float m = -INFINITY, l = 0.f;                 // raw maximum; this half's sum
 
-  if (threadIdx.x < 2) bad[threadIdx.x] = 0;
-  __syncthreads();
-  if (it0 < it1) {
-    load(it0);
-    store(it0);
+  // LDS places of this lane's operands, for tile buffer 0
+  int ka[NQ], va[k16 ? ND : 1];
+#pragma unroll
+  for (int s = 0; s < NQ; ++s) ka[s] = k_piece<RB>(lane & 31, 2 * s + hf);
+  if constexpr (k16) {
+    // transposing read: lane (i of 16) addresses row i / 4, dims 4 (i % 4).. and
+    // receives dim i of the four rows
+#pragma unroll
+    for (int b = 0; b < ND; ++b)
+      va[b] = v_piece<RB>(4 * hf + ((lane & 15) >> 2), 4 * b + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) +
+              8 * (lane & 1) + 2 * kTile;
   }
-  __syncthreads();
-  for (int it = it0; it < it1; ++it) {
-    if (it + 1 < it1) load(it + 1);
-    const int j0 = key0(it), j1 = j0 + KT - 1;
-    const bool none = r0 >= n_q || j0 > p_hi || (win && j1 <= p_lo - a.window && j0 >= a.sinks);
-    if (!none) {
-      const unsigned char* kb = smem + (it & 1) * 2 * kTile;
-      const unsigned char* vb = kb + kTile;
-      f32x16 x[NB];
+  auto read_k = [&](int buf, int nb, int s) {
+    return *reinterpret_cast<const u32x4*>(smem + ka[s] + buf * kTile + nb * 32 * RB);
+  };
+  auto read_v = [&](int buf, int t, int b) {    // 16 keys 16 t.., dims 32 b..
+    u32x4 vv;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        x[nb] = f32x16{};
+    for (int u = 0; u < 2; ++u) {
+      const u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (__attribute__((address_space(3))) s16x4*)(smem + va[b] + buf * kTile + (16 * t + 8 * u) * RB)));
+      vv[2 * u] = w[0];
+      vv[2 * u + 1] = w[1];
+    }
+    return vv;
+  };
+  auto qk = [&](const u32x4& kk, int s, f32x16 x) {
+    if constexpr (k16) return E::mfma(kk, q[s], x);
+    else {
 #pragma unroll
-        for (int s = 0; s < NQ; ++s) {
-          const u32x4 kk = *reinterpret_cast<const u32x4*>(kb + k_piece<RB>(32 * nb + (lane & 31), 2 * s + hf));
-          if constexpr (k16) {
-            x[nb] = E::mfma(kk, q[s], x[nb]);
-          } else {
+      for (int i = 0; i < 4; ++i)
+        x = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(kk[i]), __uint_as_float(q[s][i]), x, 0, 0, 0);
+      return x;
+    }
+  };
+  auto full_for = [&](int j0, int lo, int hi) {
+    const int j1 = j0 + KT - 1;
+    return j1 <= lo && (!win || j0 > hi - a.window || j1 < a.sinks);
+  };
+  auto row_max = [&](const f32x16 (&x)[NB]) {
+    float mx = x[0][0];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              x[nb] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(kk[i]), __uint_as_float(q[s][i]),
-                                                           x[nb], 0, 0, 0);
-          }
-        }
-      }
-      const bool full = j1 <= p_lo && (!win || j0 > p_hi - a.window || j1 < a.sinks);
-      auto seen = [&](int nb, int e) {
-        const int j = j0 + 32 * nb + 8 * (e >> 2) + 4 * hf + (e & 3);
-        return j <= p && (!win || j > p - a.window || j < a.sinks);
-      };
-      if (!full) {
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+      for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[nb][e]);
+    return mx;
+  };
+  // Takes a tile's maxima into m.  m follows only when some row's maximum has
+  // grown by more than 2^8, so that o is rarely rescaled: weights are then at
+  // most 2^8, which every type holds with its full relative precision.
+  auto take_max = [&](float mx) {
+    mx = fmaxf(mx, other_half(mx));
+    if (__any((mx - m) * c > 8.f)) {
+      const float mn = fmaxf(m, mx);
+      const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mn) * c);
+      l *= f;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[nb][e] = seen(nb, e) ? x[nb][e] : -INFINITY;
-      }
-      float mx = x[0][0];
+      for (int b = 0; b < ND; ++b) o[b] *= f;
+      m = mn;
+    }
+  };
+  auto mask = [&](int j0, f32x16 (&x)[NB]) {
+    // key of element e, less what the lane adds: 32 nb + 8 (e / 4) + e % 4
+    const int top = p - j0 - 4 * hf, low = top - a.window, fst = a.sinks - j0 - 4 * hf;
+    if (!(win && j0 <= p_hi - a.window)) {      // the diagonal only
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[nb][e]);
-      mx = fmaxf(mx, other_half(mx));
-      if (__any(mx > m)) {                      // some row's maximum grows: rescale
-        const float mn = fmaxf(m, mx);
-        const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mn) * c);
-        l *= f;
-#pragma unroll
-        for (int b = 0; b < ND; ++b) o[b] *= f;
-        m = mn;
-      }
-      const float mc = m == -INFINITY ? 0.f : m * c;
-      float sum = 0.f;
+        for (int e = 0; e < 16; ++e)
+          x[nb][e] = 32 * nb + 8 * (e >> 2) + (e & 3) <= top ? x[nb][e] : -INFINITY;
+    } else {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          x[nb][e] = __builtin_amdgcn_exp2f(fmaf(x[nb][e], c, -mc));
-          sum += x[nb][e];
+          const int j = 32 * nb + 8 * (e >> 2) + (e & 3);
+          x[nb][e] = j <= top && (j > low || j < fst) ? x[nb][e] : -INFINITY;
         }
-      l += sum;
-      if (full || bad[it & 1] != it + 1) {
-        if constexpr (k16) {
+    }
+  };
+
+  auto look_at_v = [&](int it, const unsigned char* vb) {
+    if (full_for(key0(it), Pa, Pb)) return;
+    // a masked key's weight is 0, but 0 * inf is not: look for such values
+    unsigned f = 0;
 #pragma unroll
-          for (int t = 0; t < 2 * NB; ++t) {
-            u32x4 pp;
+    for (int n = 0; n < kTile / (16 * kThreads); ++n) {
+      const u32x4 w = *reinterpret_cast<const u32x4*>(vb + 16 * (threadIdx.x + kThreads * n));
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              pp[i] = E::pack(x[t >> 1][8 * (t & 1) + 2 * i], x[t >> 1][8 * (t & 1) + 2 * i + 1]);
+      for (int i = 0; i < 4; ++i) f |= nonfinite_bits<TT>(w[i]);
+    }
+    if (f) redo = 1;
+  };
+
+  if (threadIdx.x == 0) redo = 0;
+  f32x16 x[NB];
+  if (it0 < it1) {                              // tile it lies in buffer (it - it0) & 1
+    copy(it0, 0, std::false_type{});
+    copy(it0, 2, std::true_type{});
+    if (it0 + 1 < it1) copy(it0 + 1, 1, std::false_type{});
+    wait_copies();
+  }
+  __syncthreads();
+  if (it0 < it1) {
 #pragma unroll
-            for (int b = 0; b < ND; ++b) {
-              // four keys of this lane's dim, twice: lane (i of 16) addresses
-              // row i / 4, dims 4 (i % 4).. and receives dim i of the four rows
-              u32x4 vv;
+    for (int nb = 0; nb < NB; ++nb) x[nb] = f32x16{};
 #pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int r = 16 * t + 8 * u + 4 * hf + ((lane & 15) >> 2);
-                const int piece = 4 * b + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-                const unsigned char* ad = vb + v_piece<RB>(r, piece) + 8 * (lane & 1);
-                const u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s16x4*)(ad)));
-                vv[2 * u] = w[0];
-                vv[2 * u + 1] = w[1];
-              }
-              o[b] = E::mfma(vv, pp, o[b]);
-            }
-          }
-        } else {
+    for (int s = 0; s < NQ; ++s) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
+      for (int nb = 0; nb < NB; ++nb) x[nb] = qk(read_k(0, nb, s), s, x[nb]);
+      PIN();
+    }
+    if (!full_for(key0(it0), p_lo, p_hi)) mask(key0(it0), x);
+    take_max(row_max(x));
+  }
+  // One tile.  xc holds its scores, masked, and m covers them.  16-bit types:
+  // the next tile's products (xn) run beside this one's exponentials, the next
+  // maxima beside P V, so that matrix cores and vector ALU work at the same
+  // time within one wavefront; the scheduling barriers keep that order.
+  auto step = [&](auto P, int it, f32x16 (&xc)[NB], f32x16 (&xn)[NB]) {
+    constexpr int b0 = decltype(P)::value, b1 = 1 - b0;
+    wait_copies();
+    __syncthreads();
+    if (it + 2 < it1) copy(it + 2, b0, std::false_type{});
+    if (it + 1 < it1) copy(it + 1, 2 + b1, std::true_type{});
+    const unsigned char* vb = smem + (2 + b0) * kTile;
+    look_at_v(it, vb);
+    const float mc = m == -INFINITY ? 0.f : m * c;
+    float sum = 0.f, mx = -INFINITY;
+    if constexpr (k16) {
+      unsigned pp[NB * 8];
+      u32x4 kc[NB];                             // K pieces, read one step ahead
 #pragma unroll
-            for (int b = 0; b < ND; ++b) {
-              const int r = 8 * (e >> 2) + 4 * hf + (e & 3), dim = 32 * b + (lane & 31);
-              const float vv = *reinterpret_cast<const float*>(vb + v_piece<RB>(r, dim >> 2) + 4 * (dim & 3));
-              o[b] = __builtin_amdgcn_mfma_f32_32x32x2f32(vv, x[0][e], o[b], 0, 0, 0);
-            }
+      for (int nb = 0; nb < NB; ++nb) {
+        xn[nb] = f32x16{};
+        kc[nb] = read_k(b1, nb, 0);
+      }
+#pragma unroll
+      for (int s = 0; s < NQ; ++s) {
+        u32x4 kn[NB];
+        if (s + 1 < NQ) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) kn[nb] = read_k(b1, nb, s + 1);
         }
-      } else {
-        // Rare: V holds infinities or NaN and some of these keys are masked.
-        // Key by key, masked keys left out; both halves need each weight.
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          for (int e = 0; e < 16; ++e) {
-            const float w0 = x[nb][0];
+        for (int nb = 0; nb < NB; ++nb) xn[nb] = qk(kc[nb], s, xn[nb]);
+        constexpr int PER = 16 * NB / NQ;
 #pragma unroll
-            for (int i = 0; i < 15; ++i) x[nb][i] = x[nb][i + 1];
-            float wr = w0;
-            if constexpr (k16) wr = TT::tof(TT::fromf(w0));
-            for (int hh = 0; hh < 2; ++hh) {
-              const int r = 32 * nb + 8 * (e >> 2) + 4 * hh + (e & 3);
-              const float w = __shfl(wr, (lane & 31) + 32 * hh);
-              const int j = j0 + r;
-              if (j <= p && (!win || j > p - a.window || j < a.sinks)) {
+        for (int u = 0; u < PER; u += 2) {
+          const int e = s * PER + u;
+          const float w0 = __builtin_amdgcn_exp2f(fmaf(xc[e >> 4][e & 15], c, -mc));
+          const float w1 = __builtin_amdgcn_exp2f(fmaf(xc[e >> 4][(e & 15) + 1], c, -mc));
+          pp[e >> 1] = E::pack(w0, w1);
+          sum += w0 + w1;
+        }
+        PIN();
+        if (s + 1 < NQ) {
 #pragma unroll
-                for (int b = 0; b < ND; ++b)
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) {
-                    const int dim = 32 * b + 8 * (i >> 2) + 4 * hf + (i & 3);
-                    constexpr int PE = 16 / (int)sizeof(S);
-                    const S v = *reinterpret_cast<const S*>(vb + v_piece<RB>(r, dim / PE) + (dim % PE) * sizeof(S));
-                    o[b][i] = fmaf(w, TT::tof(v), o[b][i]);
-                  }
-              }
-            }
-          }
+          for (int nb = 0; nb < NB; ++nb) kc[nb] = kn[nb];
         }
       }
+#pragma unroll
+      for (int t = 0; t < 2 * NB; ++t) {
+        const u32x4 w = {pp[4 * t], pp[4 * t + 1], pp[4 * t + 2], pp[4 * t + 3]};
+#pragma unroll
+        for (int b = 0; b < ND; ++b) o[b] = E::mfma(read_v(b0, t, b), w, o[b]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, xn[t >> 1][8 * (t & 1) + e]);
+        PIN();
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float w = __builtin_amdgcn_exp2f(fmaf(xc[0][e], c, -mc));
+        sum += w;
+#pragma unroll
+        for (int b = 0; b < ND; ++b) {
+          const int r = 8 * (e >> 2) + 4 * hf + (e & 3), dim = 32 * b + (lane & 31);
+          const float vv = *reinterpret_cast<const float*>(vb + v_piece<RB>(r, dim >> 2) + 4 * (dim & 3));
+          o[b] = __builtin_amdgcn_mfma_f32_32x32x2f32(vv, w, o[b], 0, 0, 0);
+        }
+        PIN();
+      }
+      xn[0] = f32x16{};
+#pragma unroll
+      for (int s = 0; s < NQ; ++s) {
+        xn[0] = qk(read_k(b1, 0, s), s, xn[0]);
+        PIN();
+      }
+      mx = row_max(xn);
     }
-    if (it + 1 < it1) store(it + 1);
-    __syncthreads();
+    l += sum;
+    if (it + 1 < it1) {
+      const int jn = key0(it + 1);
+      if (!full_for(jn, p_lo, p_hi)) {
+        mask(jn, xn);
+        mx = row_max(xn);
+      }
+      take_max(mx);
+    }
+  };
+  f32x16 y[NB];
+  for (int it = it0; it < it1; it += 2) {
+    step(std::integral_constant<int, 0>{}, it, x, y);
+    if (it + 1 >= it1) break;
+    step(std::integral_constant<int, 1>{}, it + 1, y, x);
   }
 
+  __syncthreads();
+  if (redo) {
+    redo_rows<TT, D>(a, tg, sr, r0, off, h, split, it0, it1, nS, tw0, KT);
+    return;
+  }
   l += other_half(l);
   if (row >= n_q) return;
   const int64_t i = sr.q0 + row;
