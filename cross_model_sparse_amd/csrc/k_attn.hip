@@ -144,9 +144,24 @@ constexpr int kRows = 128;                      // queries per workgroup
 // What the launch adds to the call's arguments.
 struct TileGrid {
   int ntile;                                    // row tiles (packed batch: a bound)
-  int nsplit;                                   // parts that the keys are cut into
-  float* part;                                  // [nsplit][H][N_q][D], nsplit > 1
-  float2* ml;                                   // [nsplit][H][N_q] (max, sum), log2 units
+  int len;                                      // key tiles per part; 0: one part
+  int nparts;                                   // parts of the longest row tile
+  float* part;                                  // [nparts][H][N_q][D], len > 0
+  float2* ml;                                   // [nparts][H][N_q] (max, sum), log2 units
+};
+
+// The key tiles (KT keys) that rows at positions Pa..Pb see: the sinks' tiles
+// 0..nS-1, then tiles tw0.. up to the last row's own.
+struct KeyTiles {
+  int nS, tw0, count;
+  __host__ __device__ __forceinline__ KeyTiles(int window, int sinks, int Pa, int Pb, int KT) {
+    const int kend = Pb + 1 > 0 ? Pb + 1 : 0;
+    const int first = window > 0 && Pa - window + 1 > 0 ? (Pa - window + 1) / KT : 0;
+    nS = window > 0 ? ((sinks < kend ? sinks : kend) + KT - 1) / KT : 0;
+    tw0 = first > nS ? first : nS;
+    const int rest = (kend + KT - 1) / KT - tw0;
+    count = nS + (rest > 0 ? rest : 0);
+  }
 };
 
 // Element type of the tiles: how 16-byte pieces multiply and how weights are
@@ -224,7 +239,7 @@ __device__ __forceinline__ unsigned lds_addr(const void* p) {
 // from r0 in turn.
 template <class TT, int D>
 __device__ void redo_rows(const mf::AttnArgs& a, const TileGrid& tg, const SeqRows& sr, int r0, int off,
-                          int h, int split, int it0, int it1, int nS, int tw0, int KT) {
+                          int h, int part, int it0, int it1, int nS, int tw0, int KT) {
   using S = typename TT::S;
   const int lane = threadIdx.x & 63, g = h / (a.H / a.H_kv);
   const S* K = (const S*)a.K.p + (int64_t)sr.k0 * a.K.ld + (int64_t)g * a.K.hs;
@@ -239,8 +254,8 @@ __device__ void redo_rows(const mf::AttnArgs& a, const TileGrid& tg, const SeqRo
       const int j0 = (it < nS ? it : tw0 + it - nS) * KT, j = j0 + lane;
       row.chunk(q, K, a.K.ld, V, a.V.ld, sc, j0, lane < KT && j <= p && (j >= w0 || j < a.sinks));
     }
-    if (tg.nsplit > 1) {
-      const int64_t at = ((int64_t)split * a.H + h) * a.N_q + i;
+    if (tg.len) {
+      const int64_t at = ((int64_t)part * a.H + h) * a.N_q + i;
       if (lane == 0) tg.ml[at] = make_float2(row.m, row.l);
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) tg.part[at * D + lane + 64 * c] = row.acc[c];
@@ -282,8 +297,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_tiles(const mf::AttnArgs a
     h = blockIdx.x % a.H;
     rest = blockIdx.x / a.H;
   }
-  int tile = tg.ntile - 1 - rest % tg.ntile;
-  const int split = rest / tg.ntile;
+  const int part = rest / tg.ntile;
+  int tile = tg.ntile - 1 - (rest - part * tg.ntile);
   const int g = h / (a.H / a.H_kv);
   SeqRows sr{0, a.N_q, 0, a.N_k};
   if (a.cu_q) {
@@ -303,14 +318,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_tiles(const mf::AttnArgs a
   const int off = n_k - n_q;                    // position of row 0
   const int Pa = off + R0, Pb = off + min(R0 + kRows, n_q) - 1;
 
-  // key tiles that some row of the workgroup sees
-  const int kend = max(Pb + 1, 0);
+  // key tiles that some row of the workgroup sees, and this part of them
   const bool win = a.window > 0;
-  const int nS = win ? (min(a.sinks, kend) + KT - 1) / KT : 0;
-  const int tw0 = max(win ? max(0, Pa - a.window + 1) / KT : 0, nS);
-  const int ntl = nS + max(0, (kend + KT - 1) / KT - tw0);
-  const int it0 = (int)((int64_t)ntl * split / tg.nsplit);
-  const int it1 = (int)((int64_t)ntl * (split + 1) / tg.nsplit);
+  const KeyTiles kt(a.window, a.sinks, Pa, Pb, KT);
+  const int nS = kt.nS, tw0 = kt.tw0;
+  const int it0 = tg.len ? part * tg.len : 0;
+  const int it1 = tg.len ? min(it0 + tg.len, kt.count) : kt.count;
+  if (part > 0 && it0 >= it1) return;           // whole workgroup
   auto key0 = [&](int it) { return (it < nS ? it : tw0 + it - nS) * KT; };
 
   // this wavefront's rows
@@ -499,21 +513,26 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_tiles(const mf::AttnArgs a
     float sum = 0.f, mx = -INFINITY;
     if constexpr (k16) {
       unsigned pp[NB * 8];
-      u32x4 kc[NB];                             // K pieces, read one step ahead
+      constexpr int AHEAD = 2;                  // steps that K pieces are read ahead
+      u32x4 kp[AHEAD + 1][NB], vp[2][ND];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         xn[nb] = f32x16{};
-        kc[nb] = read_k(b1, nb, 0);
+#pragma unroll
+        for (int s = 0; s < AHEAD; ++s) kp[s][nb] = read_k(b1, nb, s);
       }
 #pragma unroll
       for (int s = 0; s < NQ; ++s) {
-        u32x4 kn[NB];
-        if (s + 1 < NQ) {
+        if (s + AHEAD < NQ) {
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) kn[nb] = read_k(b1, nb, s + 1);
+          for (int nb = 0; nb < NB; ++nb) kp[(s + AHEAD) % (AHEAD + 1)][nb] = read_k(b1, nb, s + AHEAD);
+        }
+        if (s + 1 == NQ) {
+#pragma unroll
+          for (int b = 0; b < ND; ++b) vp[0][b] = read_v(b0, 0, b);
         }
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) xn[nb] = qk(kc[nb], s, xn[nb]);
+        for (int nb = 0; nb < NB; ++nb) xn[nb] = qk(kp[s % (AHEAD + 1)][nb], s, xn[nb]);
         constexpr int PER = 16 * NB / NQ;
 #pragma unroll
         for (int u = 0; u < PER; u += 2) {
@@ -524,37 +543,50 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_tiles(const mf::AttnArgs a
           sum += w0 + w1;
         }
         PIN();
-        if (s + 1 < NQ) {
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) kc[nb] = kn[nb];
-        }
       }
 #pragma unroll
       for (int t = 0; t < 2 * NB; ++t) {
+        if (t + 1 < 2 * NB) {
+#pragma unroll
+          for (int b = 0; b < ND; ++b) vp[(t + 1) & 1][b] = read_v(b0, t + 1, b);
+        }
         const u32x4 w = {pp[4 * t], pp[4 * t + 1], pp[4 * t + 2], pp[4 * t + 3]};
 #pragma unroll
-        for (int b = 0; b < ND; ++b) o[b] = E::mfma(read_v(b0, t, b), w, o[b]);
+        for (int b = 0; b < ND; ++b) o[b] = E::mfma(vp[t & 1][b], w, o[b]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) mx = fmaxf(mx, xn[t >> 1][8 * (t & 1) + e]);
         PIN();
       }
     } else {
+      // one V column element a lane and step, K pieces: both read ahead
+      auto read_vf = [&](int e, int b) {
+        const int r = 8 * (e >> 2) + 4 * hf + (e & 3), dim = 32 * b + (lane & 31);
+        return *reinterpret_cast<const float*>(vb + v_piece<RB>(r, dim >> 2) + 4 * (dim & 3));
+      };
+      float vp[2][ND];
+#pragma unroll
+      for (int b = 0; b < ND; ++b) vp[0][b] = read_vf(0, b);
+      u32x4 kp[2];
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
+        if (e + 1 < 16) {
+#pragma unroll
+          for (int b = 0; b < ND; ++b) vp[(e + 1) & 1][b] = read_vf(e + 1, b);
+        } else {
+          kp[0] = read_k(b1, 0, 0);
+        }
         const float w = __builtin_amdgcn_exp2f(fmaf(xc[0][e], c, -mc));
         sum += w;
 #pragma unroll
-        for (int b = 0; b < ND; ++b) {
-          const int r = 8 * (e >> 2) + 4 * hf + (e & 3), dim = 32 * b + (lane & 31);
-          const float vv = *reinterpret_cast<const float*>(vb + v_piece<RB>(r, dim >> 2) + 4 * (dim & 3));
-          o[b] = __builtin_amdgcn_mfma_f32_32x32x2f32(vv, w, o[b], 0, 0, 0);
-        }
+        for (int b = 0; b < ND; ++b)
+          o[b] = __builtin_amdgcn_mfma_f32_32x32x2f32(vp[e & 1][b], w, o[b], 0, 0, 0);
         PIN();
       }
       xn[0] = f32x16{};
 #pragma unroll
       for (int s = 0; s < NQ; ++s) {
-        xn[0] = qk(read_k(b1, 0, s), s, xn[0]);
+        if (s + 1 < NQ) kp[(s + 1) & 1] = read_k(b1, 0, s + 1);
+        xn[0] = qk(kp[s & 1], s, xn[0]);
         PIN();
       }
       mx = row_max(xn);
@@ -578,14 +610,14 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_tiles(const mf::AttnArgs a
 
   __syncthreads();
   if (redo) {
-    redo_rows<TT, D>(a, tg, sr, r0, off, h, split, it0, it1, nS, tw0, KT);
+    redo_rows<TT, D>(a, tg, sr, r0, off, h, part, it0, it1, nS, tw0, KT);
     return;
   }
   l += other_half(l);
   if (row >= n_q) return;
   const int64_t i = sr.q0 + row;
-  if (tg.nsplit > 1) {
-    const int64_t at = ((int64_t)split * a.H + h) * a.N_q + i;
+  if (tg.len) {
+    const int64_t at = ((int64_t)part * a.H + h) * a.N_q + i;
     if (hf == 0) tg.ml[at] = make_float2(m == -INFINITY ? -INFINITY : m * c, l);
     float* op = tg.part + at * D + 4 * hf;
 #pragma unroll
@@ -615,26 +647,29 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_tiles(const mf::AttnArgs a
     }
 }
 
-// Joins the parts of split keys in part order; one wavefront per (query, head).
+// Joins a row's parts in part order; one wavefront per (query, head).
 template <class TT, int D>
-__global__ __launch_bounds__(256) void k_attn_join(const mf::AttnArgs a, const TileGrid tg) {
+__global__ __launch_bounds__(256) void k_attn_join(const mf::AttnArgs a, const TileGrid tg, int KT) {
   using S = typename TT::S;
   constexpr int NE = D / 64;
   const int lane = threadIdx.x & 63;
   const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int h = blockIdx.y;
   if (i >= a.N_q) return;
+  const int R0 = (int)i / kRows * kRows, off = a.N_k - a.N_q;
+  const KeyTiles kt(a.window, a.sinks, off + R0, off + min(R0 + kRows, a.N_q) - 1, KT);
+  const int np = max(1, (kt.count + tg.len - 1) / tg.len);
+  const int64_t step = (int64_t)a.H * a.N_q, at = (int64_t)h * a.N_q + i;
   float m = -INFINITY, l = 0.f, acc[NE] = {};
-  for (int s = 0; s < tg.nsplit; ++s) m = fmaxf(m, tg.ml[((int64_t)s * a.H + h) * a.N_q + i].x);
+  for (int s = 0; s < np; ++s) m = fmaxf(m, tg.ml[at + s * step].x);
   const float mu = m == -INFINITY ? 0.f : m;
-  for (int s = 0; s < tg.nsplit; ++s) {
-    const int64_t at = ((int64_t)s * a.H + h) * a.N_q + i;
-    const float2 ml = tg.ml[at];
+#pragma unroll 4
+  for (int s = 0; s < np; ++s) {
+    const float2 ml = tg.ml[at + s * step];
     const float f = __builtin_amdgcn_exp2f(ml.x - mu);
     l += ml.y * f;
-    if (ml.y == 0.f) continue;                  // no key of this part is visible
 #pragma unroll
-    for (int c = 0; c < NE; ++c) acc[c] = fmaf(tg.part[at * D + NE * lane + c], f, acc[c]);
+    for (int c = 0; c < NE; ++c) acc[c] = fmaf(tg.part[(at + s * step) * D + NE * lane + c], f, acc[c]);
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   S* o = (S*)a.O + i * a.ldO + (int64_t)h * D + NE * lane;
@@ -648,25 +683,35 @@ bool rows16(const void* p, int64_t ld, int64_t hs, int es) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * es) % 16 == 0 && (hs * es) % 16 == 0;
 }
 
-// Parts that the keys of a call are cut into: with fewer row tiles than half
-// the CUs hold workgroups (two each), enough parts to fill them, each of at
-// least kMinPart key tiles.
-constexpr int kMinPart = 4;
-int split_of(int H, int N_q, int N_k, int KT, int window, int sinks) {
-  const int64_t wgs = (int64_t)H * ((N_q + kRows - 1) / kRows);
-  if (wgs > 256) return 1;
-  int64_t keys = N_k;
-  if (window > 0) keys = std::min<int64_t>(keys, (int64_t)window + sinks + kRows);
-  const int64_t tiles = (keys + KT - 1) / KT;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({(512 + wgs - 1) / wgs, tiles / kMinPart, 64}));
+// Few row tiles (at most one workgroup a CU): keys are cut into parts of one
+// length, so that the parts, about four a CU, are equally long whatever the
+// mask makes of the rows; a part has at least 4 tiles (fp32: 2, whose tiles take
+// as long).
+void split_of(TileGrid& tg, int dt, int H, int N_q, int N_k, int window, int sinks) {
+  tg.len = 0;
+  tg.nparts = 1;
+  const int KT = dt == MF_F32 ? 32 : 64, ntile = (N_q + kRows - 1) / kRows;
+  if ((int64_t)H * ntile > 256) return;
+  int64_t work = 0;
+  int longest = 0;
+  for (int t = 0; t < ntile; ++t) {
+    const int Pa = N_k - N_q + t * kRows, Pb = N_k - N_q + std::min((t + 1) * kRows, N_q) - 1;
+    const KeyTiles kt(window, sinks, Pa, Pb, KT);
+    work += kt.count;
+    longest = std::max(longest, kt.count);
+  }
+  const int len = (int)std::max<int64_t>(dt == MF_F32 ? 2 : 4, (work * H + 1023) / 1024);
+  if (longest <= len) return;
+  tg.len = len;
+  tg.nparts = (longest + len - 1) / len;
 }
 
 template <class TT, int D>
 hipError_t run_tiles(const mf::AttnArgs& a, const TileGrid& tg, hipStream_t st) {
-  const int64_t wgs = (int64_t)tg.ntile * a.H * tg.nsplit;
+  const int64_t wgs = (int64_t)tg.ntile * a.H * tg.nparts;
   k_attn_tiles<TT, D><<<(unsigned)wgs, kThreads, 0, st>>>(a, tg);
-  if (tg.nsplit > 1)
-    k_attn_join<TT, D><<<dim3((a.N_q + 3) / 4, a.H), 256, 0, st>>>(a, tg);
+  if (tg.len)
+    k_attn_join<TT, D><<<dim3((a.N_q + 3) / 4, a.H), 256, 0, st>>>(a, tg, sizeof(typename TT::S) == 2 ? 64 : 32);
   return hipGetLastError();
 }
 
@@ -679,7 +724,7 @@ hipError_t run_plain(const mf::AttnArgs& a, hipStream_t st) {
 }
 
 template <class TT>
-hipError_t run(mf::AttnArgs a, void* ws, size_t ws_bytes, size_t need, int KT, hipStream_t st) {
+hipError_t run(int dt, mf::AttnArgs a, void* ws, size_t ws_bytes, size_t need, hipStream_t st) {
   constexpr int es = sizeof(typename TT::S);
   // a window that reaches every key is none; bounds the kernels' sums too
   if (a.window >= a.N_k) a.window = 0;
@@ -691,11 +736,11 @@ hipError_t run(mf::AttnArgs a, void* ws, size_t ws_bytes, size_t need, int KT, h
   if (!tiles) return run_plain<TT>(a, st);
   TileGrid tg{};
   tg.ntile = a.cu_q ? a.N_q / kRows + a.S : (a.N_q + kRows - 1) / kRows;
-  tg.nsplit = 1;
-  if (!a.cu_q && need > 0 && ws && ws_bytes >= need) {
-    tg.nsplit = split_of(a.H, a.N_q, a.N_k, KT, a.window, a.sinks);
+  tg.nparts = 1;
+  if (need > 0 && ws && ws_bytes >= need) {
+    split_of(tg, dt, a.H, a.N_q, a.N_k, a.window, a.sinks);
     tg.part = (float*)ws;
-    tg.ml = (float2*)(tg.part + (int64_t)tg.nsplit * a.H * a.N_q * a.d);
+    tg.ml = (float2*)(tg.part + (int64_t)tg.nparts * a.H * a.N_q * a.d);
   }
   return a.d == 64 ? run_tiles<TT, 64>(a, tg, st) : run_tiles<TT, 128>(a, tg, st);
 }
@@ -706,16 +751,17 @@ namespace mf {
 
 size_t attention_split_bytes(int dt, int H, int, int N_q, int N_k, int d, int window, int sinks) {
   if (window >= N_k) window = 0;
-  const int ns = split_of(H, N_q, N_k, dt == MF_F32 ? 32 : 64, window, std::min(sinks, N_k));
-  return ns > 1 ? (size_t)ns * H * N_q * ((size_t)d * 4 + 8) : 0;
+  TileGrid tg{};
+  split_of(tg, dt, H, N_q, N_k, window, std::min(sinks, N_k));
+  return tg.len ? (size_t)tg.nparts * H * N_q * ((size_t)d * 4 + 8) : 0;
 }
 
 hipError_t launch_attention(int dt, const AttnArgs& a, void* ws, size_t ws_bytes, hipStream_t st) {
   const size_t need = a.cu_q || a.N_k == 0
       ? 0 : attention_split_bytes(dt, a.H, a.H_kv, a.N_q, a.N_k, a.d, a.window, a.sinks);
-  if (dt == MF_F32) return run<TF32>(a, ws, ws_bytes, need, 32, st);
-  if (dt == MF_F16) return run<TF16>(a, ws, ws_bytes, need, 64, st);
-  return run<TBF16>(a, ws, ws_bytes, need, 64, st);
+  if (dt == MF_F32) return run<TF32>(dt, a, ws, ws_bytes, need, st);
+  if (dt == MF_F16) return run<TF16>(dt, a, ws, ws_bytes, need, st);
+  return run<TBF16>(dt, a, ws, ws_bytes, need, st);
 }
 
 }  // namespace mf
