@@ -146,6 +146,7 @@ struct TileGrid {
   int ntile;                                    // row tiles (packed batch: a bound)
   int len;                                      // key tiles per part; 0: one part
   int nparts;                                   // parts of the longest row tile
+  int total;                                    // workgroups per head
   float* part;                                  // [nparts][H][N_q][D], len > 0
   float2* ml;                                   // [nparts][H][N_q] (max, sum), log2 units
 };
@@ -297,8 +298,39 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_tiles(const mf::AttnArgs a
     h = blockIdx.x % a.H;
     rest = blockIdx.x / a.H;
   }
-  const int part = rest / tg.ntile;
-  int tile = tg.ntile - 1 - (rest - part * tg.ntile);
+  int tile = tg.ntile - 1 - rest, part = 0;
+  if (tg.len) {
+    // Workgroup `rest` of the head among all row tiles' parts: counted by a
+    // scan over the tiles, 64 at a time.  (A grid with room for the longest
+    // tile's parts at every tile would leave gaps, and a CU that took an empty
+    // workgroup does not take another's place in the dispatcher's round.)
+    int before = 0;
+    for (int t0 = 0;; t0 += 64) {
+      const int t = tg.ntile - 1 - t0 - lane;
+      int n = 0;
+      if (t >= 0) {
+        const int P0 = a.N_k - a.N_q + t * kRows, P1 = a.N_k - a.N_q + min((t + 1) * kRows, a.N_q) - 1;
+        n = max(1, (KeyTiles(a.window, a.sinks, P0, P1, KT).count + tg.len - 1) / tg.len);
+      }
+      int incl = n;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int u = __shfl_up(incl, d);
+        if (lane >= d) incl += u;
+      }
+      const int all = __builtin_amdgcn_readlane(incl, 63);
+      if (rest < before + all || t0 + 64 >= tg.ntile) {
+        const int at = __ffsll((unsigned long long)__ballot(rest < before + incl)) - 1;
+        if (at < 0) return;                     // behind the last part
+        tile = tg.ntile - 1 - t0 - at;
+        part = rest - before - __shfl(incl - n, at);
+        break;
+      }
+      before += all;
+    }
+    tile = __builtin_amdgcn_readfirstlane(tile);
+    part = __builtin_amdgcn_readfirstlane(part);
+  }
   const int g = h / (a.H / a.H_kv);
   SeqRows sr{0, a.N_q, 0, a.N_k};
   if (a.cu_q) {
@@ -324,7 +356,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_tiles(const mf::AttnArgs a
   const int nS = kt.nS, tw0 = kt.tw0;
   const int it0 = tg.len ? part * tg.len : 0;
   const int it1 = tg.len ? min(it0 + tg.len, kt.count) : kt.count;
-  if (part > 0 && it0 >= it1) return;           // whole workgroup
   auto key0 = [&](int it) { return (it < nS ? it : tw0 + it - nS) * KT; };
 
   // this wavefront's rows
@@ -582,6 +613,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_tiles(const mf::AttnArgs a
           o[b] = __builtin_amdgcn_mfma_f32_32x32x2f32(vp[e & 1][b], w, o[b], 0, 0, 0);
         PIN();
       }
+      if (it + 1 >= it1) {
+        l += sum;
+        return;
+      }
       xn[0] = f32x16{};
 #pragma unroll
       for (int s = 0; s < NQ; ++s) {
@@ -660,17 +695,26 @@ __global__ __launch_bounds__(256) void k_attn_join(const mf::AttnArgs a, const T
   const KeyTiles kt(a.window, a.sinks, off + R0, off + min(R0 + kRows, a.N_q) - 1, KT);
   const int np = max(1, (kt.count + tg.len - 1) / tg.len);
   const int64_t step = (int64_t)a.H * a.N_q, at = (int64_t)h * a.N_q + i;
+  // a part a lane for the statistics
   float m = -INFINITY, l = 0.f, acc[NE] = {};
-  for (int s = 0; s < np; ++s) m = fmaxf(m, tg.ml[at + s * step].x);
-  const float mu = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
-  for (int s = 0; s < np; ++s) {
-    const float2 ml = tg.ml[at + s * step];
-    const float f = __builtin_amdgcn_exp2f(ml.x - mu);
-    l += ml.y * f;
+  for (int s = lane; s < np; s += 64) m = fmaxf(m, tg.ml[at + s * step].x);
 #pragma unroll
-    for (int c = 0; c < NE; ++c) acc[c] = fmaf(tg.part[(at + s * step) * D + NE * lane + c], f, acc[c]);
+  for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+  const float mu = m == -INFINITY ? 0.f : m;
+  for (int s0 = 0; s0 < np; s0 += 64) {
+    const float2 ml = s0 + lane < np ? tg.ml[at + (s0 + lane) * step] : make_float2(-INFINITY, 0.f);
+    const float fl = __builtin_amdgcn_exp2f(ml.x - mu);
+    l = fmaf(ml.y, fl, l);
+    const int n = min(64, np - s0);
+#pragma unroll 8
+    for (int s = 0; s < n; ++s) {
+      const float f = __shfl(fl, s);
+#pragma unroll
+      for (int c = 0; c < NE; ++c) acc[c] = fmaf(tg.part[(at + (s0 + s) * step) * D + NE * lane + c], f, acc[c]);
+    }
   }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) l += __shfl_xor(l, d);
   const float inv = l == 0.f ? 0.f : 1.f / l;
   S* o = (S*)a.O + i * a.ldO + (int64_t)h * D + NE * lane;
 #pragma unroll
@@ -683,32 +727,49 @@ bool rows16(const void* p, int64_t ld, int64_t hs, int es) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * es) % 16 == 0 && (hs * es) % 16 == 0;
 }
 
-// Few row tiles (at most one workgroup a CU): keys are cut into parts of one
-// length, so that the parts, about four a CU, are equally long whatever the
-// mask makes of the rows; a part has at least 4 tiles (fp32: 2, whose tiles take
-// as long).
-void split_of(TileGrid& tg, int dt, int H, int N_q, int N_k, int window, int sinks) {
+// Few row tiles (at most one workgroup a CU): the keys may be cut into parts of
+// one length, equally long whatever the mask makes of the rows.  The length is
+// the one that an estimate of the time likes best: rounds of workgroups (one a
+// CU, two where tiles leave the matrix cores gaps: 16-bit types) times a part's
+// tiles and start, and the parts' way through memory to the join.  Measured on
+// d = 128: 1.4 us a tile (two workgroups a CU), fp32 4.3 us; a start is about
+// 5 us; 8 heads of 1000 fp32 queries 151 us whole, 44 us in parts.
+void split_of(TileGrid& tg, int dt, int H, int N_q, int N_k, int d, int window, int sinks) {
   tg.len = 0;
   tg.nparts = 1;
-  const int KT = dt == MF_F32 ? 32 : 64, ntile = (N_q + kRows - 1) / kRows;
+  tg.total = (N_q + kRows - 1) / kRows;
+  const int KT = dt == MF_F32 ? 32 : 64, ntile = tg.total;
   if ((int64_t)H * ntile > 256) return;
-  int64_t work = 0;
+  int count[256];
   int longest = 0;
   for (int t = 0; t < ntile; ++t) {
     const int Pa = N_k - N_q + t * kRows, Pb = N_k - N_q + std::min((t + 1) * kRows, N_q) - 1;
-    const KeyTiles kt(window, sinks, Pa, Pb, KT);
-    work += kt.count;
-    longest = std::max(longest, kt.count);
+    count[t] = KeyTiles(window, sinks, Pa, Pb, KT).count;
+    longest = std::max(longest, count[t]);
   }
-  const int len = (int)std::max<int64_t>(dt == MF_F32 ? 2 : 4, (work * H + 1023) / 1024);
-  if (longest <= len) return;
-  tg.len = len;
-  tg.nparts = (longest + len - 1) / len;
+  const double us = (dt == MF_F32 ? 4.3 : 1.4) * d / 128, start = 5.0;
+  const int slots = dt == MF_F32 ? 256 : 512;
+  double best = start + us * longest;
+  static const int cuts[] = {2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 48, 64, 96, 128, 192, 256};
+  for (const int k : cuts) {
+    const int len = (longest + k - 1) / k;
+    if (len < 2) break;
+    int64_t parts = 0;
+    for (int t = 0; t < ntile; ++t) parts += std::max(1, (count[t] + len - 1) / len);
+    const int64_t rounds = (parts * H + slots - 1) / slots;
+    const double t = rounds * (start + us * len) + 6.0 + parts * H * (kRows * d * 8 / 4.5e6);
+    if (t < best) {
+      best = t;
+      tg.len = len;
+      tg.nparts = (longest + len - 1) / len;
+      tg.total = (int)parts;
+    }
+  }
 }
 
 template <class TT, int D>
 hipError_t run_tiles(const mf::AttnArgs& a, const TileGrid& tg, hipStream_t st) {
-  const int64_t wgs = (int64_t)tg.ntile * a.H * tg.nparts;
+  const int64_t wgs = (int64_t)tg.total * a.H;
   k_attn_tiles<TT, D><<<(unsigned)wgs, kThreads, 0, st>>>(a, tg);
   if (tg.len)
     k_attn_join<TT, D><<<dim3((a.N_q + 3) / 4, a.H), 256, 0, st>>>(a, tg, sizeof(typename TT::S) == 2 ? 64 : 32);
@@ -737,8 +798,9 @@ hipError_t run(int dt, mf::AttnArgs a, void* ws, size_t ws_bytes, size_t need, h
   TileGrid tg{};
   tg.ntile = a.cu_q ? a.N_q / kRows + a.S : (a.N_q + kRows - 1) / kRows;
   tg.nparts = 1;
+  tg.total = tg.ntile;
   if (need > 0 && ws && ws_bytes >= need) {
-    split_of(tg, dt, a.H, a.N_q, a.N_k, a.window, a.sinks);
+    split_of(tg, dt, a.H, a.N_q, a.N_k, a.d, a.window, a.sinks);
     tg.part = (float*)ws;
     tg.ml = (float2*)(tg.part + (int64_t)tg.nparts * a.H * a.N_q * a.d);
   }
@@ -752,7 +814,7 @@ namespace mf {
 size_t attention_split_bytes(int dt, int H, int, int N_q, int N_k, int d, int window, int sinks) {
   if (window >= N_k) window = 0;
   TileGrid tg{};
-  split_of(tg, dt, H, N_q, N_k, window, std::min(sinks, N_k));
+  split_of(tg, dt, H, N_q, N_k, d, window, std::min(sinks, N_k));
   return tg.len ? (size_t)tg.nparts * H * N_q * ((size_t)d * 4 + 8) : 0;
 }
 
