@@ -63,7 +63,7 @@ struct PartGrid {
   int slots;                                    // score entries per (sequence, head)
   float* part;                                  // [S][nparts][H][D]
   float2* ml;                                   // [S][nparts][H] (max, sum), log2 units
-  float* score;                                 // [S][H][slots], log2 units; null without mass
+  float* score;                                 // [S][H][slots], log2 units, the last unit spare
 };
 
 // The visible tiles of a sequence, tiles of KT keys: the sinks' tiles
@@ -96,7 +96,8 @@ __device__ __forceinline__ void wave_order() {
 }
 
 // kWhole: a tile never straddles pages (page is a multiple of the tile).
-template <class TT, int D, bool kWhole>
+// kMass: the scores stay in the workspace for the weights.
+template <class TT, int D, bool kWhole, bool kMass>
 __global__ __launch_bounds__(kThreads, 2) void k_decode_parts(const mf::DecodeArgs a, const PartGrid pg) {
   using S = typename TT::S;
   constexpr bool k16 = sizeof(S) == 2;
@@ -192,7 +193,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_parts(const mf::DecodeAr
 #pragma unroll
   for (int b = 0; b < NB; ++b) o[b] = f32x4{0.f, 0.f, 0.f, 0.f};
   float m = -INFINITY, l = 0.f;
-  float* score = pg.score ? pg.score + ((int64_t)s * a.H + h) * pg.slots : nullptr;
+  float* score = kMass ? pg.score + ((int64_t)s * a.H + h) * pg.slots : nullptr;
 
   auto step = [&](int it, KTile& cur, KTile& nxt) {
     const unsigned vm = __builtin_amdgcn_readfirstlane(cur.vm);
@@ -231,10 +232,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_parts(const mf::DecodeAr
         x[nt][i] *= c;
         mx = fmaxf(mx, x[nt][i]);
       }
-    if (score && col < nh) {
+    if constexpr (kMass) {
+      // Every lane stores, those of the padding heads to a spare place: with a
+      // known number of younger stores the waits for loads need not wait for
+      // them too (a store behind a branch cost the batch of 64 a quarter).
+      float* to = score + (col < nh ? it * KT : pg.slots - kUnit) + 4 * grp;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        *reinterpret_cast<f32x4*>(score + it * KT + 16 * nt + 4 * grp) = x[nt];
+      for (int nt = 0; nt < NT; ++nt) *reinterpret_cast<f32x4*>(to + 16 * nt) = x[nt];
     }
     mx = fmaxf(mx, __shfl_xor(mx, 16));
     mx = fmaxf(mx, __shfl_xor(mx, 32));
@@ -336,6 +340,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_parts(const mf::DecodeAr
   }
 }
 
+#ifndef WANT
+#define WANT 512
+#endif
 constexpr int kMassKeys = 1024;                 // keys per workgroup of the weights
 constexpr int kMaxParts = 1024;
 
@@ -414,33 +421,60 @@ __global__ __launch_bounds__(kThreads) void k_decode_join(const mf::DecodeArgs a
   }
   const int j0 = (chunk - G) * kMassKeys;
   if (j0 >= len) return;
+  // four consecutive rows a thread: tiles hold a multiple of four.  The first
+  // heads' scores are in flight while the log-sum-exps are formed.
+  const int j = j0 + 4 * t;
+  const int tile = j / KT;
+  const int it = tile < tl.nS ? tile : tile - tl.tw0 + tl.nS;
+  const bool listed = j < tl.n && (tile < tl.nS || tile >= tl.tw0);
+  const float* score = pg.score + ((int64_t)s * a.H + (int64_t)g * G) * pg.slots +
+                       (listed ? it * KT + (j - tile * KT) : 0);
+  auto scores_of = [&](int hh) { return *reinterpret_cast<const f32x4*>(score + (int64_t)hh * pg.slots); };
+  constexpr int NH = 4;
+  f32x4 x[NH];
+#pragma unroll
+  for (int i = 0; i < NH; ++i) x[i] = scores_of(min(i, G - 1));
+  const int64_t mrow = ((int64_t)s * a.H_kv + g) * a.ldmass + j;
+  float w[4] = {};
+  if (a.mass_in) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = j + i < len ? a.mass_in[mrow + i] : 0.f;
+  }
   for (int hh = wave; hh < G; hh += kWaves) {
     float M = -INFINITY, L = 0.f;
     for (int p = lane; p < np; p += 64) M = fmaxf(M, pg.ml[at0 + (int64_t)p * a.H + hh].x);
     M = all_max(M);
     const float mu = M == -INFINITY ? 0.f : M;
     for (int p = lane; p < np; p += 64) {
-      const float2 x = pg.ml[at0 + (int64_t)p * a.H + hh];
-      L = fmaf(x.y, __builtin_amdgcn_exp2f(x.x - mu), L);
+      const float2 y = pg.ml[at0 + (int64_t)p * a.H + hh];
+      L = fmaf(y.y, __builtin_amdgcn_exp2f(y.x - mu), L);
     }
     L = all_sum(L);
     // +infinity: no key of this head is visible, every weight is 0
     if (lane == 0) lse2[hh] = L == 0.f ? INFINITY : M + log2f(L);
   }
   __syncthreads();
-  const float* score = pg.score + ((int64_t)s * a.H + (int64_t)g * G) * pg.slots;
-  const int64_t mrow = ((int64_t)s * a.H_kv + g) * a.ldmass;
-  for (int j = j0 + t; j < min(j0 + kMassKeys, len); j += kThreads) {
-    const int tile = j / KT;
-    const int it = tile < tl.nS ? tile : tile - tl.tw0 + tl.nS;
-    float w = 0.f;
-    if (j < tl.n && (j >= tl.w0 || j < a.sinks))
-      for (int hh = 0; hh < G; ++hh) {
-        const float x = score[(int64_t)hh * pg.slots + it * KT + (j - tile * KT)];
-        w += x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x - lse2[hh]);
-      }
-    a.mass_out[mrow + j] = (a.mass_in ? a.mass_in[mrow + j] : 0.f) + w;
+  float sum[4] = {};
+  for (int h0 = 0; h0 < G; h0 += NH) {
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+      if (h0 + i >= G) break;
+      const float L = lse2[h0 + i];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        sum[e] += x[i][e] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x[i][e] - L);
+    }
+#pragma unroll
+    for (int i = 0; i < NH; ++i)
+      if (h0 + NH < G) x[i] = scores_of(min(h0 + NH + i, G - 1));
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (j + i < len) {
+      const int ji = j + i;
+      const bool vis = listed && ji < tl.n && (ji >= tl.w0 || ji < a.sinks);
+      a.mass_out[mrow + i] = w[i] + (vis ? sum[i] : 0.f);
+    }
 }
 
 // 32-key units that the longest sequence can see
@@ -457,7 +491,7 @@ PartGrid part_grid(int S, int max_len, int H, int H_kv, int window, int sinks) {
   PartGrid pg{};
   const int64_t u = std::max<int64_t>(1, max_units(max_len, window, sinks));
   const int64_t rows = (int64_t)S * H_kv * ((H / H_kv + 15) / 16);
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>((1024 + rows - 1) / rows, u / (2 * kWaves)));
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>((WANT + rows - 1) / rows, u / (2 * kWaves)));
   pg.units = (int)((u + want - 1) / want);
   pg.nparts = (int)((u + pg.units - 1) / pg.units);
   pg.slots = (int)((u + 1) * kUnit);
@@ -475,8 +509,13 @@ hipError_t run(const mf::DecodeArgs& a, void* ws, hipStream_t st) {
     if (a.mass_out) pg.score = (float*)(pg.ml + (((int64_t)a.S * pg.nparts * a.H + 1) & ~int64_t(1)));
   }
   const dim3 grid(a.S, a.H_kv * ((a.H / a.H_kv + 15) / 16), pg.nparts);
-  if (a.c.page % KT == 0) k_decode_parts<TT, D, true><<<grid, kThreads, 0, st>>>(a, pg);
-  else k_decode_parts<TT, D, false><<<grid, kThreads, 0, st>>>(a, pg);
+  if (a.c.page % KT == 0) {
+    if (a.mass_out) k_decode_parts<TT, D, true, true><<<grid, kThreads, 0, st>>>(a, pg);
+    else k_decode_parts<TT, D, true, false><<<grid, kThreads, 0, st>>>(a, pg);
+  } else {
+    if (a.mass_out) k_decode_parts<TT, D, false, true><<<grid, kThreads, 0, st>>>(a, pg);
+    else k_decode_parts<TT, D, false, false><<<grid, kThreads, 0, st>>>(a, pg);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !join) return e;
   const int chunks = a.mass_out ? (a.c.max_len + kMassKeys - 1) / kMassKeys : 0;
