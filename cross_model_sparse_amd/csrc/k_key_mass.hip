@@ -63,6 +63,9 @@ __global__ __launch_bounds__(64) void k_key_mass_plain(const mf::KeyMassArgs a) 
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
+#ifndef TARGET
+#define TARGET 4096
+#endif
 
 struct Runs {
   int len;                                      // queries per run, a multiple of 64
@@ -275,7 +278,7 @@ Runs runs_of(int dt, int H, int N_q, int N_k) {
   Runs rn{};
   const int block = dt == MF_F32 ? 32 * kWaves : 64 * kWaves;
   rn.blocks = (N_k + block - 1) / block;
-  const int64_t len = ((int64_t)N_q * H * rn.blocks + 4095) / 4096;
+  const int64_t len = ((int64_t)N_q * H * rn.blocks + TARGET - 1) / TARGET;
   rn.len = (int)std::min<int64_t>(8192, std::max<int64_t>(64, (len + 63) / 64 * 64));
   rn.count = (N_q + rn.len - 1) / rn.len;
   return rn;
