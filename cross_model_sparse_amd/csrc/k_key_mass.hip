@@ -18,6 +18,8 @@
 // k_key_mass_plain: one thread per (KV head, key).  Any alignment.
 #include "mf_attn.h"
 
+#include <math.h>
+
 #include <algorithm>
 #include <type_traits>
 
@@ -63,9 +65,6 @@ __global__ __launch_bounds__(64) void k_key_mass_plain(const mf::KeyMassArgs a) 
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-#ifndef TARGET
-#define TARGET 4096
-#endif
 
 struct Runs {
   int len;                                      // queries per run, a multiple of 64
@@ -272,14 +271,30 @@ bool rows16(const mf::Strided& x, int es) {
   return reinterpret_cast<uintptr_t>(x.p) % 16 == 0 && (x.ld * es) % 16 == 0 && (x.hs * es) % 16 == 0;
 }
 
-// Runs of queries: about 4096 workgroups (eight for each that runs at a time,
-// for causal masks leave half of them short), at most 8192 queries each.
-Runs runs_of(int dt, int H, int N_q, int N_k) {
+// Length of the runs of queries, at most 8192.  Every run costs a start (keys
+// into registers, the first tile's latency) and the last ones leave CUs idle for
+// half a run: with W queries in all, over heads and key blocks, the sum of both
+// is least near sqrt(W).  Measured around it (d = 128, bf16): N = 2048, 32 heads
+// 42 us with 512 queries, 50 with 256, 48 with 1024; window 1024 at N = 8192, 32
+// heads 178 us with 1024, 216 with 2048, 340 with 4096; N = 8192, 40 heads,
+// causal within 4% from 1280 to 5120.
+Runs runs_of(int dt, int H, int N_q, int N_k, int window, int sinks) {
   Runs rn{};
   const int block = dt == MF_F32 ? 32 * kWaves : 64 * kWaves;
   rn.blocks = (N_k + block - 1) / block;
-  const int64_t len = ((int64_t)N_q * H * rn.blocks + TARGET - 1) / TARGET;
-  rn.len = (int)std::min<int64_t>(8192, std::max<int64_t>(64, (len + 63) / 64 * 64));
+  // W from at most 64 of the key blocks
+  const int n = std::min(rn.blocks, 64);
+  double seen = 0;
+  for (int i = 0; i < n; ++i) {
+    const int64_t j0 = (int64_t)rn.blocks * i / n * block;
+    int64_t q = std::min<int64_t>(N_q, N_k - j0);
+    if (window > 0 && j0 >= sinks) q = std::min<int64_t>(q, (int64_t)window + block);
+    seen += (double)q;
+  }
+  if (n > 0) seen *= (double)rn.blocks / n;
+  const int64_t len = (int64_t)sqrt(0.65 * seen * H);
+  rn.len = (int)std::min<int64_t>(8192, (len + 63) / 64 * 64);
+  rn.len = std::max(rn.len, 64);
   rn.count = (N_q + rn.len - 1) / rn.len;
   return rn;
 }
@@ -310,7 +325,7 @@ hipError_t run(int dt, mf::KeyMassArgs a, void* ws, hipStream_t st) {
   if (a.window >= a.N_k) a.window = 0;          // reaches every key
   a.sinks = std::min(a.sinks, a.N_k);
   if (!rows16(a.Q, es) || !rows16(a.K, es)) return run_plain<TT>(a, st);
-  Runs rn = runs_of(dt, a.H, a.N_q, a.N_k);
+  Runs rn = runs_of(dt, a.H, a.N_q, a.N_k, a.window, a.sinks);
   rn.part = (float*)ws;
   return a.d == 64 ? run_tiles<TT, 64>(a, rn, st) : run_tiles<TT, 128>(a, rn, st);
 }
@@ -319,8 +334,9 @@ hipError_t run(int dt, mf::KeyMassArgs a, void* ws, hipStream_t st) {
 
 namespace mf {
 
-size_t key_mass_workspace_bytes(int dt, int H, int, int N_q, int N_k, int, int, int) {
-  const Runs rn = runs_of(dt, H, N_q, N_k);
+size_t key_mass_workspace_bytes(int dt, int H, int, int N_q, int N_k, int, int window, int sinks) {
+  if (window >= N_k) window = 0;
+  const Runs rn = runs_of(dt, H, N_q, N_k, window, std::min(sinks, N_k));
   return (size_t)H * rn.count * N_k * 4;
 }
 
