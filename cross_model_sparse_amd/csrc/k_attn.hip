@@ -14,9 +14,21 @@
 // one exchange with lane l ^ 32, rescaling is a multiplication by a lane's own
 // factor, and exp(S)^T is already the next product's operand: with keys taken
 // in the order in which the lane holds them, P never moves between lanes.
-// K and V tiles (64 keys; 32 in fp32) pass through registers into two LDS
-// buffers while the tile before is computed; 16-byte pieces are XOR-swizzled
-// so that both LDS reads are free of bank conflicts without padding.
+// K and V tiles (64 keys; 32 in fp32) are copied straight into two LDS buffers
+// each, a tile ahead (K two); 16-byte pieces are XOR-swizzled so that both LDS
+// reads are free of bank conflicts without padding.
+// A weight is rounded to the storage type before it multiplies V (the matrix
+// instruction takes one type; a second product for the rest would cost half of
+// the time again); sums, maxima and accumulators are fp32.
+//
+// Bound by the matrix cores together with the vector ALU: 32 products, 32
+// exponentials and about 120 other vector instructions for a wavefront's 32 x 64
+// tile at d = 128, which overlap within one wavefront and between the two of a
+// SIMD (counters: matrix cores 48% busy, vector ALU 43%, LDS 24%, at 1.9 GHz
+// under the load).  Measured, 32 heads, 8 KV heads, d = 128, bf16, causal:
+// N = 32768 8.2 to 8.5 ms (1035 to 1077 TFLOP/s; an 8192^3 library product
+// reaches 1188), N = 8192 560 us (980), window 1024 at N = 8192 177 us (728 of
+// the visible pairs; the tiles' own pairs are 20% more).
 //
 // k_attn_plain: one wavefront per (query, head), 64 keys at a time, one key a
 // lane for the scores and two dims a lane for the output.  Any alignment.
@@ -649,9 +661,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_tiles(const mf::AttnArgs a
     return;
   }
   l += other_half(l);
-  if (row >= n_q) return;
   const int64_t i = sr.q0 + row;
   if (tg.len) {
+    if (row >= n_q) return;
     const int64_t at = ((int64_t)part * a.H + h) * a.N_q + i;
     if (hf == 0) tg.ml[at] = make_float2(m == -INFINITY ? -INFINITY : m * c, l);
     float* op = tg.part + at * D + 4 * hf;
@@ -664,22 +676,42 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_tiles(const mf::AttnArgs a
     return;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  if (a.lse && hf == 0)
+  if (a.lse && hf == 0 && row < n_q)
     a.lse[(int64_t)h * a.N_q + i] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * kLn2f;
-  S* op = (S*)a.O + i * a.ldO + (int64_t)h * D + 4 * hf;
+  if constexpr (k16) {
+    // A lane holds four dims at a time of its own row: through LDS (each
+    // wavefront its own part of the tiles' buffers, which nobody reads any
+    // more) to whole rows, 16 bytes a lane.
+    unsigned char* ob = smem + wave * kTile;
+    const int rl = lane & 31;
 #pragma unroll
-  for (int b = 0; b < ND; ++b)
+    for (int b = 0; b < ND; ++b)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if constexpr (k16) {
-        *reinterpret_cast<u32x2*>(op + 32 * b + 8 * e) =
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<u32x2*>(ob + k_piece<RB>(rl, 4 * b + e) + 8 * hf) =
             u32x2{E::pack(o[b][4 * e] * inv, o[b][4 * e + 1] * inv),
                   E::pack(o[b][4 * e + 2] * inv, o[b][4 * e + 3] * inv)};
-      } else {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+    for (int n = 0; n < 32 / (64 / CH); ++n) {
+      const int r = lane / CH + 64 / CH * n, cc = lane % CH;
+      const u32x4 w = *reinterpret_cast<const u32x4*>(ob + k_piece<RB>(r, cc));
+      if (r0 + r < n_q)
+        *reinterpret_cast<u32x4*>((S*)a.O + (int64_t)(sr.q0 + r0 + r) * a.ldO + (int64_t)h * D +
+                                  cc * (16 / (int)sizeof(S))) = w;
+    }
+  } else {
+    if (row >= n_q) return;
+    S* op = (S*)a.O + i * a.ldO + (int64_t)h * D + 4 * hf;
+#pragma unroll
+    for (int b = 0; b < ND; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
         *reinterpret_cast<f32x4*>(op + 32 * b + 8 * e) =
             f32x4{o[b][4 * e] * inv, o[b][4 * e + 1] * inv, o[b][4 * e + 2] * inv, o[b][4 * e + 3] * inv};
-      }
-    }
+  }
 }
 
 // Joins a row's parts in part order; one wavefront per (query, head).

