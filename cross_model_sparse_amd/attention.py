@@ -68,6 +68,13 @@ def _code(t: torch.Tensor) -> int:
     return c
 
 
+def _ints(**xs) -> None:
+    """Sizes that the C boundary takes as int (ctypes would cut them silently)."""
+    for name, x in xs.items():
+        if not -(1 << 31) <= x < 1 << 31:
+            _bad(f"{name} = {x} does not fit 32 bits")
+
+
 def _full(t: torch.Tensor | None, name: str, shape: tuple, dtype, where: int) -> None:
     """t (if given) is a contiguous tensor of that shape, type and device."""
     if t is None:
@@ -248,6 +255,7 @@ def attention_window(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: t
     [N_q][H][d], lse float32 [H][N_q] (-inf for a query that sees nothing)."""
     rows, H, H_kv, N_q, N_k, d = _attn_shapes(Q, K, V, scale)
     code = _code(Q)
+    _ints(window=window, sinks=sinks, N_q=N_q, N_k=N_k)
     ctx, handle = _on(Q.device, stream)
     with ctx:
         out, lse, ldO = _attn_out(Q, H, N_q, d, out, lse)
@@ -272,6 +280,7 @@ def attention_window_varlen(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
     S = cu_q.shape[0] - 1 if cu_q.dim() == 1 else -1
     if S < 0:
         _bad("cu_q must be an int32 [S+1] tensor")
+    _ints(window=window, sinks=sinks, N_q=N_q, N_k=N_k)
     _full(cu_q, "cu_q", (S + 1,), torch.int32, Q.get_device())
     _full(cu_k, "cu_k", (S + 1,), torch.int32, Q.get_device())
     ctx, handle = _on(Q.device, stream)
@@ -286,6 +295,7 @@ def attention_window_varlen(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
 def _cache(K, V, lens, block_table, S, max_len):
     if K.dim() != 4 or not K.is_contiguous():
         _bad("K must be a contiguous [n_pages][H_kv][page][d] pool")
+    _ints(max_len=max_len)
     where = K.get_device()
     _full(V, "V", K.shape, K.dtype, where)
     n_pages, H_kv, page, d = K.shape
@@ -325,6 +335,7 @@ def attention_decode(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, lens: to
     S, H, d = Q.shape
     cache, H_kv, dk = _cache(K, V, lens, block_table, S, max_len)
     dev, where = K.device, K.get_device()
+    _ints(window=window, sinks=sinks)
     _same(where, K.dtype, Q, "Q")
     _full(scale, "scale", (H,), torch.float32, where)
     if dk != d or (S and H > 1 and Q.stride(1) != d):
@@ -383,6 +394,7 @@ def key_mass_qk(Q: torch.Tensor, K: torch.Tensor, scale: torch.Tensor, lse: torc
     code = _code(Q)
     if dk != d:
         _bad("K must match Q in d")
+    _ints(window=window, sinks=sinks, N_q=N_q, N_k=N_k)
     _same(where, Q.dtype, K, "K")
     _full(scale, "scale", (H,), torch.float32, where)
     _full(lse, "lse", (H, N_q), torch.float32, where)
@@ -429,6 +441,7 @@ def cache_evict(mass: torch.Tensor, K: torch.Tensor, V: torch.Tensor, lens: torc
     _full(K_out, "K_out", (S, H_kv, cap, d), K.dtype, where)
     _full(V_out, "V_out", (S, H_kv, cap, d), K.dtype, where)
     _full(mass_out, "mass_out", (S, H_kv, cap), torch.float32, where)
+    _ints(budget=budget, sinks=sinks, recent=recent)
     if budget < 1:
         _bad(f"budget must be >= 1 (got {budget})")
     ctx, handle = _on(dev, stream)

@@ -346,15 +346,29 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_tiles(const mf::AttnArgs a
   const int g = h / (a.H / a.H_kv);
   SeqRows sr{0, a.N_q, 0, a.N_k};
   if (a.cu_q) {
+    sr = SeqRows{0, 0, 0, 0};
+    int first = 0;
     // sequence s owns row tiles cu_q[s]/kRows + s and up: at least as many as
-    // it needs, and the next sequence starts behind them
-    int lo = 0, hi = a.S - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (min(max(a.cu_q[mid], 0), a.N_q) / kRows + mid <= tile) lo = mid; else hi = mid - 1;
+    // it needs, and the next sequence starts behind them.  A sequence a lane, so
+    // that all offsets are one load apart.
+    for (int s0 = 0; s0 < a.S; s0 += 64) {
+      const int s = s0 + lane;
+      SeqRows mine{0, 0, 0, 0};
+      if (s < a.S) mine = seq_rows(a, s);
+      const uint64_t from = __ballot(s < a.S && mine.q0 / kRows + s <= tile);
+      if (from == 0) break;                     // a later sequence's first
+      const int at = 63 - __clzll((long long)from);
+      sr.q0 = __shfl(mine.q0, at);
+      sr.q1 = __shfl(mine.q1, at);
+      sr.k0 = __shfl(mine.k0, at);
+      sr.k1 = __shfl(mine.k1, at);
+      first = sr.q0 / kRows + s0 + at;
     }
-    sr = seq_rows(a, lo);
-    tile -= sr.q0 / kRows + lo;
+    sr.q0 = __builtin_amdgcn_readfirstlane(sr.q0);
+    sr.q1 = __builtin_amdgcn_readfirstlane(sr.q1);
+    sr.k0 = __builtin_amdgcn_readfirstlane(sr.k0);
+    sr.k1 = __builtin_amdgcn_readfirstlane(sr.k1);
+    tile -= __builtin_amdgcn_readfirstlane(first);
   }
   const int n_q = sr.q1 - sr.q0, n_k = sr.k1 - sr.k0;
   const int R0 = tile * kRows;

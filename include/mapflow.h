@@ -633,10 +633,10 @@ size_t mf_attention_split_workspace_bytes(int dtype, int H, int H_kv, int N_q, i
  * cu_q[s] .. cu_q[s+1]-1 of Q, O and lse and rows cu_k[s] .. cu_k[s+1]-1 of K
  * and V, each with its own positions.
  *  S            host, number of sequences, >= 0.
- *  cu_q, cu_k   device, [S+1] int32, nondecreasing from 0.
+ *  cu_q, cu_k   device, [S+1] int32, nondecreasing, cu[0] >= 0.
  *  N_q, N_k     host, rows of Q and K/V; they size the grid and bound every
- *               access, whatever the tables hold.  Rows of O and lse behind the
- *               last sequence are left as they were.
+ *               access, whatever the tables hold.  Rows of O and lse before the
+ *               first sequence and behind the last are left as they were.
  *  Errors: as mf_attention_window, and MF_ERR_INVALID for S < 0.
  */
 int mf_attention_window_varlen(int S, const int32_t* cu_q, const int32_t* cu_k, const void* Q,

@@ -322,6 +322,14 @@ def test_binding_refuses_shapes_and_types():
         lambda: mf.attention_decode(q3, pool, pool, lens, sc, 8, block_table=lens),
         lambda: mf.attention_decode(q3, pool, pool, lens, sc, 8, mass_in=h(2, 2, 8)),
         lambda: mf.attention_decode(q3, pool, pool, lens, sc, 8, mass_out=h(2, 3, 8)),
+        # sizes that an int would cut: 2^32 + 5 is not a window of 5
+        lambda: mf.attention_window(Q, K, V, sc, window=(1 << 32) + 5),
+        lambda: mf.attention_window_varlen(Q, K, V, sc, lens, lens, sinks=1 << 31),
+        lambda: mf.attention_decode(q3, pool, pool, lens, sc, (1 << 32) + 8),
+        lambda: mf.attention_decode(q3, pool, pool, lens, sc, 8, window=1 << 40),
+        lambda: mf.key_mass_qk(Q, K, sc, h(4, 8), window=1 << 33),
+        lambda: mf.cache_evict(h(2, 2, 8), pool, pool, lens, (1 << 32) + 4),
+        lambda: mf.cache_evict(h(2, 2, 8), pool, pool, lens, 4, recent=1 << 32),
         lambda: mf.key_mass_qk(Q, K, sc, h(4, 9)),
         lambda: mf.key_mass_qk(Q, K, sc, h(4, 8), mass_in=h(4, 8)),
         lambda: mf.cache_evict(h(2, 3, 8), pool, pool, lens, 4),

@@ -102,6 +102,24 @@ def test_many_packed_sequences(gpu):
         assert torch.equal(O[a:b], one[0]) and torch.equal(lse[:, a:b], one[1])
 
 
+def test_packed_batch_that_starts_behind_row_0(gpu):
+    """Offsets need not start at 0: rows before the first sequence stay as they were."""
+    g = gen(14)
+    N, H, Hk, d = 700, 2, 1, 64
+    Q, K, V = (randn(g, s, "bf16").to(gpu) for s in ((H, N, d), (Hk, N, d), (N, Hk, d)))
+    sc = torch.full((H,), 0.1, device=gpu)
+    cu = torch.tensor([300, 300, 420, 650], dtype=torch.int32, device=gpu)
+    O = torch.full((N, H, d), 5.0, dtype=torch.bfloat16, device=gpu)
+    lse = torch.full((H, N), 5.0, device=gpu)
+    mf.attention_window_varlen(Q, K, V, sc, cu, cu, out=O, lse=lse)
+    for a, b in ((300, 420), (420, 650)):
+        one = mf.attention_window(Q[:, a:b], K[:, a:b], V[a:b], sc,
+                                  workspace=torch.empty(16, dtype=torch.uint8, device=gpu))
+        assert torch.equal(O[a:b], one[0]) and torch.equal(lse[:, a:b], one[1])
+    for a, b in ((0, 300), (650, N)):
+        assert (O[a:b] == 5.0).all() and (lse[:, a:b] == 5.0).all()
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
 def test_decode_masked_rows_hold_anything(gpu, dt):
     g = gen(5)
