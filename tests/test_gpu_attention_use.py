@@ -145,6 +145,73 @@ def test_decode_masked_rows_hold_anything(gpu, dt):
         close(host(mo)[s, :, :n], want, want * 2 * mass_rel(r, d) + 1e-30, "mass")
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_decode_of_a_fused_projection_into_a_wider_buffer(gpu, dt):
+    g = gen(15)
+    S, H, Hk, d, L = 5, 6, 2, 64, 130
+    x = randn(g, (S, H + 3, d), dt).to(gpu)
+    K, V = randn(g, (S, Hk, L, d), dt).to(gpu), randn(g, (S, Hk, L, d), dt).to(gpu)
+    sc, lens = torch.full((H,), 0.2, device=gpu), torch.tensor([130, 1, 64, 65, 0], dtype=torch.int32, device=gpu)
+    big = torch.full((S, H + 1, d), 3.0, dtype=DT[dt], device=gpu)
+    a = mf.attention_decode(x[:, 1:1 + H], K, V, lens, sc, L, out=big[:, 1:])
+    b = mf.attention_decode(x[:, 1:1 + H].contiguous(), K, V, lens, sc, L)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and (big[:, 0] == 3.0).all()
+    # off 16 bytes: queries and outputs need their element's alignment only
+    off = torch.zeros(S * H * d + 1, dtype=DT[dt], device=gpu)
+    off[1:] = x[:, 1:1 + H].reshape(-1)
+    o2 = torch.zeros(S * H * d + 1, dtype=DT[dt], device=gpu)
+    c = mf.attention_decode(off[1:].view(S, H, d), K, V, lens, sc, L, out=o2[1:].view(S, H, d))
+    assert torch.equal(c[0], b[0]) and float(o2[0]) == 0.0
+
+
+def test_one_bad_query_or_sequence_stays_alone(gpu):
+    """A NaN query, and a sequence full of NaN, leave their neighbours as they were."""
+    g = gen(16)
+    N, H, Hk, d = 200, 4, 2, 128
+    Q, K, V = (randn(g, s, "bf16").to(gpu) for s in ((H, N, d), (Hk, N, d), (N, Hk, d)))
+    sc = torch.full((H,), 0.1, device=gpu)
+    cu = torch.tensor([0, 70, 130, N], dtype=torch.int32, device=gpu)
+    want = mf.attention_window_varlen(Q, K, V, sc, cu, cu)
+    Q2, K2, V2 = Q.clone(), K.clone(), V.clone()
+    K2[:, 70:130], V2[70:130], Q2[1, 30] = float("nan"), float("nan"), float("nan")
+    got = mf.attention_window_varlen(Q2, K2, V2, sc, cu, cu)
+    keep = torch.ones(N, H, dtype=torch.bool, device=gpu)
+    keep[70:130], keep[30, 1] = False, False
+    assert torch.equal(got[0][keep], want[0][keep]) and torch.equal(got[1][keep.t()], want[1][keep.t()])
+    assert torch.isnan(got[0][~keep].float()).all()
+    pool, vpool = K[None].contiguous(), V.transpose(0, 1)[None].contiguous()
+    lens = torch.tensor([N, N], dtype=torch.int32, device=gpu)
+    two = torch.cat([pool, pool]), torch.cat([vpool, vpool])
+    q = Q[:, -2:].transpose(0, 1).contiguous()
+    want = mf.attention_decode(q, *two, lens, sc, N)
+    two[0][1], two[1][1], q[0, 2] = float("nan"), float("nan"), float("nan")
+    got = mf.attention_decode(q, *two, lens, sc, N)
+    ok = [0, 1, 3]
+    assert torch.equal(got[0][0, ok], want[0][0, ok]) and torch.isnan(got[0][1].float()).all()
+    assert torch.isnan(got[0][0, 2].float()).all()
+
+
+def test_the_documented_sequence_of_calls(gpu):
+    """The README's example."""
+    g = gen(17)
+    N, H, Hk, d = 2000, 8, 2, 128
+    x = randn(g, (N, H + 2 * Hk, d), "bf16").to(gpu)
+    q, k, V = x[:, :H], x[:, H:H + Hk], x[:, H + Hk:]
+    wq = wk = torch.ones(d, dtype=torch.bfloat16, device=gpu)
+    positions = torch.arange(N, dtype=torch.int32, device=gpu)
+    scale = torch.full((H,), d ** -0.5, device=gpu)
+    lens = torch.tensor([N], dtype=torch.int32, device=gpu)
+    freq, af = mf.rope_frequencies(128, 1e6, "yarn", 4.0, orig_len=4096)
+    Q, K = mf.qk_norm_rope(q, k, freq.cuda(), positions, wq=wq, wk=wk, attn_factor=af)
+    O, lse = mf.attention_window(Q, K, V, scale, window=1024, sinks=4)
+    mass = mf.key_mass_qk(Q, K, scale, lse, window=1024, sinks=4)
+    kept, lens, Kc, Vc, m = mf.cache_evict(mass[None], K[None], V.transpose(0, 1)[None].contiguous(), lens,
+                                           budget=512, sinks=4, recent=64)
+    assert O.shape == (N, H, d) and lens.tolist() == [512] and Kc.shape == (1, Hk, 512, d)
+    # every query's weights add up to 1
+    assert torch.allclose(mass.sum(), torch.tensor(float(H * N), device=gpu), rtol=1e-3)
+
+
 def test_decode_of_empty_caches(gpu):
     Q = torch.randn(3, 4, 64, device=gpu).half()
     K = torch.zeros(3, 2, 16, 64, device=gpu, dtype=torch.float16)
