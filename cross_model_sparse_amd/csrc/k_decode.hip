@@ -67,7 +67,9 @@ struct PartGrid {
   int slots;                                    // score entries per (sequence, head)
   float* part;                                  // [S][nparts][H][D]
   float2* ml;                                   // [S][nparts][H] (max, sum), log2 units
-  float* score;                                 // [S][H][slots], log2 units, the last unit spare
+  // [S][16 heads of a group][tiles][heads][keys of a tile], log2 units, the last
+  // unit spare; a tile's heads lie together, so that it leaves in one run
+  float* score;
 };
 
 // The visible tiles of a sequence, tiles of KT keys: the sinks' tiles
@@ -155,15 +157,22 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_parts(const mf::DecodeAr
   const char* Kp = (const char*)a.c.K;
   const char* Vp = (const char*)a.c.V;
   constexpr unsigned kAll = KT == 32 ? 0xffffffffu : 0xffffu;
-  auto load = [&](int it, KTile& t) {
+  // Pool page of a tile (kWhole), fetched a step before the tile's rows.  The
+  // table is constant during the call: a scalar load, which waits for no store.
+  auto page_of = [&](int it) -> int64_t {
+    if (!kWhole || it >= t1) return -1;
+    const int64_t slot = (int64_t)s * a.c.max_pages + tl.key0(it, KT) / a.c.page;
+    return a.c.table ? (int64_t)((__attribute__((address_space(4))) const int32_t*)(uintptr_t)a.c.table)[slot] : slot;
+  };
+  auto load = [&](int it, int64_t page, KTile& t) {
     const int j0 = tl.key0(it, KT);
     const int lj = j0 + (lane & (KT - 1));      // the key this lane answers for
     bool vis = lj < tl.n && (lj >= tl.w0 || lj < a.sinks);
     if constexpr (kWhole) {
-      const int64_t base = cache_row(a.c, s, j0, g, a.H_kv, D);
-      vis = vis && base >= 0;
+      const bool there = page >= 0 && page < a.c.n_pages;
+      vis = vis && there;
       t.vm = (unsigned)__ballot(vis) & kAll;
-      const int64_t b = (base >= 0 ? base : 0) * ES;
+      const int64_t b = there ? ((page * a.H_kv + g) * a.c.page + j0 % a.c.page) * (int64_t)(D * ES) : 0;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -197,8 +206,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_parts(const mf::DecodeAr
 #pragma unroll
   for (int b = 0; b < NB; ++b) o[b] = f32x4{0.f, 0.f, 0.f, 0.f};
   float m = -INFINITY, l = 0.f;
-  float* score = kMass ? pg.score + ((int64_t)s * a.H + h) * pg.slots : nullptr;
+  float* score = kMass ? pg.score + ((int64_t)s * a.H + h0) * pg.slots : nullptr;
 
+  int64_t page = page_of(t0 + wave);
   auto step = [&](int it, KTile& cur, KTile& nxt) {
     const unsigned vm = __builtin_amdgcn_readfirstlane(cur.vm);
     wave_order();                               // the last tile's reads are done
@@ -210,7 +220,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_parts(const mf::DecodeAr
       *reinterpret_cast<u32x4*>(vb + v_piece<ES, RB>(r, lane % CH)) = w;
     }
     wave_order();
-    if (it + kWaves < t1) load(it + kWaves, nxt);
+    if (it + kWaves < t1) load(it + kWaves, page, nxt);
+    page = page_of(it + 2 * kWaves);
     f32x4 x[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -239,7 +250,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_parts(const mf::DecodeAr
     if constexpr (kMass) {
       // Every lane stores, those of the padding heads to a spare place: no
       // branch between the stores and the waits for older loads.
-      float* to = score + (col < nh ? it * KT : pg.slots - kUnit) + 4 * grp;
+      float* to = score + (int64_t)(col < nh ? it * KT : pg.slots - kUnit) * nh +
+                  (col < nh ? col : 0) * KT + 4 * grp;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) *reinterpret_cast<f32x4*>(to + 16 * nt) = x[nt];
     }
@@ -298,7 +310,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_parts(const mf::DecodeAr
 
   KTile ka, kb;
   int it = t0 + wave;
-  if (it < t1) load(it, ka);
+  if (it < t1) load(it, page, ka);
+  page = page_of(it + kWaves);
   while (it < t1) {
     step(it, ka, kb);
     it += kWaves;
@@ -427,9 +440,12 @@ __global__ __launch_bounds__(kThreads) void k_decode_join(const mf::DecodeArgs a
   const int tile = j / KT;
   const int it = tile < tl.nS ? tile : tile - tl.tw0 + tl.nS;
   const bool listed = j < tl.n && (tile < tl.nS || tile >= tl.tw0);
-  const float* score = pg.score + ((int64_t)s * a.H + (int64_t)g * G) * pg.slots +
-                       (listed ? it * KT + (j - tile * KT) : 0);
-  auto scores_of = [&](int hh) { return *reinterpret_cast<const f32x4*>(score + (int64_t)hh * pg.slots); };
+  const float* score = pg.score + ((int64_t)s * a.H + (int64_t)g * G) * pg.slots + (listed ? j - tile * KT : 0);
+  auto scores_of = [&](int hh) {
+    const int h0 = hh & ~15, nh = min(16, G - h0);
+    return *reinterpret_cast<const f32x4*>(score + (int64_t)h0 * pg.slots + (int64_t)(listed ? it * KT : 0) * nh +
+                                           (hh - h0) * KT);
+  };
   constexpr int NH = 4;
   f32x4 x[NH];
 #pragma unroll
