@@ -33,8 +33,6 @@ def _bad(msg: str):
     raise MapflowError(MF_ERR_INVALID, msg)
 
 
-
-
 _NULL = contextlib.nullcontext()
 
 
@@ -139,24 +137,26 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, freq: torch.Tensor | None,
     With slots (int64 [N]) k goes to row slots[n] of the cache pool K and v to
     that of V, pools [n_pages][H_k][page][d] (mf_qk_norm_rope_cache); slots
     outside the pool are skipped.  Returns (Q, K, V)."""
-    _rows3(q, "q")
-    _rows3(k, "k")
+    if q.dim() != 3 or k.dim() != 3:
+        _bad("q and k must have three dims")
     N, H_q, d = q.shape
     H_k = k.shape[1]
     dev, dt, where = q.device, q.dtype, q.get_device()
     code = _code(q)
-    if k.shape[0] != N or k.shape[2] != d:
-        _bad("k must match q in N and d")
     if layout not in _LAYOUT:
         _bad(f"unknown layout {layout!r}")
-    for t, name, H in ((q, "q", H_q), (k, "k", H_k), (v, "v", H_k)):
-        if t is None:
-            continue
+
+    def source(t, name, H):                      # checked; its stride from row to row
         _same(where, dt, t, name)
         if t.shape != (N, H, d):
             _bad(f"{name} must be [{N}][{H}][{d}]")
-        if N and ((H > 1 and t.stride(1) != d) or t.stride(2) != 1):
+        n, h, e = t.stride()
+        if N and ((H > 1 and h != d) or e != 1):
             _bad(f"{name}'s heads must lie side by side")
+        return n if N > 1 else H * d
+
+    ldq, ldk = source(q, "q", H_q), source(k, "k", H_k)
+    ldv = 0 if v is None else source(v, "v", H_k)
     _same(where, dt, Q, "Q")
     _same(where, dt, K, "K")
     rot = 0 if freq is None else 2 * freq.shape[0]
@@ -169,21 +169,19 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, freq: torch.Tensor | None,
     _full(wk, "wk", (d,), dt, where)
     ctx, handle = _on(dev, stream)
 
-    def lead(t):                                 # stride from row to row
-        return t.stride(0) if N > 1 else t.shape[1] * d
-
     def out(t, H, name):
         shape = (N, H, d) if token_major else (H, N, d)
         if t is None:
             t = torch.empty(shape, dtype=dt, device=dev)
-        elif t.shape != shape or (t.numel() and t.stride(2) != 1):
+            return (t, H * d, d) if token_major else (t, d, N * d)
+        if t.shape != shape or (t.numel() and t.stride(2) != 1):
             _bad(f"{name} must be {list(shape)} with contiguous rows")
         n, h = (0, 1) if token_major else (1, 0)
         return t, (t.stride(n) if N > 1 else H * d), (t.stride(h) if H > 1 else d)
 
     with ctx:
         Q, ldQ, hsQ = out(Q, H_q, "Q")
-        head = (code, N, d, _p(q), H_q, lead(q), _p(k), H_k, lead(k))
+        head = (code, N, d, _p(q), H_q, ldq, _p(k), H_k, ldk)
         norm = (_p(wq), _p(wk), float(eps), _p(freq), rot, _LAYOUT[layout], float(attn_factor),
                 _p(positions), _p(Q), ldQ, hsQ)
         if slots is None:
@@ -198,7 +196,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, freq: torch.Tensor | None,
         if K.dim() != 4 or K.shape[1] != H_k or K.shape[3] != d or not K.is_contiguous():
             _bad("K must be a contiguous [n_pages][H_k][page][d] pool")
         _full(V, "V", K.shape, dt, where)
-        _check(load().mf_qk_norm_rope_cache(*head, _p(v), lead(v), *norm, _p(slots), _p(K), _p(V),
+        _check(load().mf_qk_norm_rope_cache(*head, _p(v), ldv, *norm, _p(slots), _p(K), _p(V),
                                             K.shape[0], K.shape[2], handle))
         return Q, K, V
 
