@@ -763,6 +763,8 @@ int mf_cache_evict(const float* mass, int64_t ldmass, const void* K, const void*
   MF_REQUIRE(K_out != K && K_out != V && V_out != K && V_out != V && K_out != V_out,
              "an output pool is a source pool or the other output");
   MF_REQUIRE(mass_out != mass || !mass, "mass_out is mass");
+  // every head of a sequence reads its length while one of them writes the new one
+  MF_REQUIRE(lens_out != lens, "lens_out is lens");
   return mf::hip_check(mf::launch_evict(dtype, a, (hipStream_t)stream), "mf_cache_evict launch");
 }
 

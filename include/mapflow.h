@@ -716,9 +716,11 @@ int mf_key_mass_qk(const void* Q, int64_t ldQ, int64_t hsQ, const void* K, int64
  *            from n on.
  *  kept      device, [S][H_kv][budget] int32: kept rows, -1 from n on.
  *  lens_out  device, [S] int32, or NULL: n.
+ *  mass_out, kept and lens_out must not overlap the inputs.
  *  Errors: MF_ERR_INVALID for null pointers, negative sizes, budget < 1, sinks
  *  + recent > budget, cap_out < budget, bad d, H_kv or dtype, max_len >
- *  max_pages*page, misaligned pools, an output pool equal to a source pool.
+ *  max_pages*page, misaligned pools, an output pool equal to a source pool,
+ *  mass_out equal to mass, lens_out equal to lens.
  */
 int mf_cache_evict(const float* mass, int64_t ldmass, const void* K, const void* V, int64_t n_pages,
                    int page, const int32_t* block_table, int max_pages, const int32_t* lens,

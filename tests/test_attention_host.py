@@ -282,6 +282,12 @@ def test_evict_refusals(L, kw, frag):
     assert evict(L, S=0, mass=None, kept=None, Ko=None, Vo=None, lens=None, K=None, V=None) == mf.MF_OK
 
 
+def test_evict_refuses_lengths_written_in_place(L):
+    # one head's workgroup would write lens[s] while the others still read it
+    assert evict(L, lo=FAKE) == INV
+    assert "lens_out is lens" in last(L)
+
+
 # ---- refusals of the binding ---------------------------------------------------
 
 def test_binding_refuses_host_tensors():
